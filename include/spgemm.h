@@ -59,7 +59,8 @@ typedef enum {
   SPG_ERR_TIMEOUT = 6            /* a kernel gave up on a bounded wait */
 } spg_status;
 
-typedef enum { SPG_F16 = 0, SPG_BF16 = 1, SPG_S8 = 2 } spg_dtype;
+/* SPG_F32 is a type of the layer norm entry points only. */
+typedef enum { SPG_F16 = 0, SPG_BF16 = 1, SPG_S8 = 2, SPG_F32 = 3 } spg_dtype;
 
 enum { SPG_OUT_F16 = 0, SPG_OUT_S32 = 1 };  /* spgemm_24_s8 output modes */
 enum { SPG_X_MK = 0, SPG_X_KM = 1 };        /* spgemm_tw_f16 activation layouts */
@@ -386,6 +387,56 @@ spg_status spgemm_tw_f32(const float* X, int64_t ldx, int x_layout, const spg_tw
  * ------------------------------------------------------------------------- */
 spg_status spgemm_tw_f16_noalloc(const void* X, int64_t ldx, const spg_tw_desc* desc, void* Y, int64_t ldy,
                                  int64_t M, spg_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * layernorm, layernorm_s8, layernorm_bwd  (no counterpart on the pages: the
+ * norm in front of a transformer's pruned layers, whose output is their X)
+ *
+ *   h  = X, or X + res rounded to `dtype` and written to H (the residual sum
+ *        of a transformer block; the norm is taken of the rounded sum)
+ *   mu = mean_c h,  r = 1 / sqrt(mean_c (h - mu)^2 + eps)
+ *   y  = (h - mu) r gamma + beta
+ *   layernorm:    Y  = y, one round-to-nearest-even to `dtype`
+ *   layernorm_s8: Yq = clamp(rne(y * qscale), -127, 127), the int8 activations
+ *                 of spgemm_24_s8 (whose scale[] carries 1 / qscale); a NaN
+ *                 gives code 0
+ * All sums and statistics are fp32, the variance from the differences to the
+ * mean.  A NaN or infinity in a row stays in that row.
+ *   X    [M, C] of `dtype` (SPG_F16, SPG_BF16 or SPG_F32), pitch ldx >= C
+ *   res  [M, C], pitch ldres, and H [M, C], pitch ldh: both or neither (NULL)
+ *   gamma, beta [C] of wdtype, which is `dtype` or SPG_F32; beta may be NULL (0)
+ *   Y    [M, C] of `dtype`, pitch ldy; Yq int8 [M, C], pitch ldy
+ *   mean, rstd fp32 [M]: mu and r of each row for layernorm_bwd, or NULL
+ * H and Y may be the same memory as X or res (same pointer and pitch), but not
+ * as each other.  layernorm_bwd, with z = (h - mu) r and g = dY gamma:
+ *   dX = r (g - mean_c g - z mean_c(g z)) (+ dH), one rounding to `dtype`
+ *   dgamma[c] = sum_m dY z,  dbeta[c] = sum_m dY, summed in fp32 in a fixed
+ *   order, one rounding to wdtype
+ *   X    the h that the norm was taken of (H where there was a residual)
+ *   dH   [M, C] or NULL: the gradient that reaches h by the residual path
+ *   dX   [M, C]; may be the same memory as dY or dH (same pointer and pitch)
+ *   dgamma, dbeta [C] of wdtype; dbeta may be NULL.  M == 0 writes zeros.
+ *   workspace 16-byte aligned, ws_bytes >= layernorm_bwd_workspace_size; its
+ *   contents are scratch, and calls that may overlap need one each.
+ * Limits: 1 <= C <= 16384, 0 <= M < 2^31, 0 <= eps.  Pointers aligned to their
+ * element; any pitch.  Rows that all start on 16-byte boundaries are read and
+ * written in 16-byte vectors, others element by element.
+ * ------------------------------------------------------------------------- */
+spg_status layernorm(const void* X, int64_t ldx, const void* res, int64_t ldres, void* H, int64_t ldh,
+                     const void* gamma, const void* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd,
+                     int64_t M, int64_t C, spg_dtype dtype, spg_dtype wdtype, spg_stream_t stream);
+
+spg_status layernorm_s8(const void* X, int64_t ldx, const void* res, int64_t ldres, void* H, int64_t ldh,
+                        const void* gamma, const void* beta, float eps, float qscale, int8_t* Yq, int64_t ldy,
+                        int64_t M, int64_t C, spg_dtype dtype, spg_dtype wdtype, spg_stream_t stream);
+
+/* Workspace bytes of layernorm_bwd on the current device (0 for M == 0 or sizes outside the limits). */
+size_t layernorm_bwd_workspace_size(int64_t M, int64_t C, spg_dtype dtype);
+
+spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, const float* mean,
+                         const float* rstd, const void* gamma, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                         void* dgamma, void* dbeta, void* workspace, size_t ws_bytes, int64_t M, int64_t C,
+                         spg_dtype dtype, spg_dtype wdtype, spg_stream_t stream);
 
 #ifdef __cplusplus
 }

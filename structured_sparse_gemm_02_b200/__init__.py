@@ -16,7 +16,7 @@ from typing import Optional, Sequence
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspgemm.so")
 
-SPG_F16, SPG_BF16, SPG_S8 = 0, 1, 2
+SPG_F16, SPG_BF16, SPG_S8, SPG_F32 = 0, 1, 2, 3
 SPG_OUT_F16, SPG_OUT_S32 = 0, 1
 SPG_X_MK, SPG_X_KM = 0, 1
 SPG_ACT_NONE, SPG_ACT_GELU = 0, 1
@@ -69,6 +69,13 @@ SIGNATURES = {
     "spgemm_tw_f32": (ctypes.c_int, [_p, _i64, ctypes.c_int, ctypes.POINTER(SpgTwDesc), _p, _p, _i64, _i64, _p, _sz,
                                      _p]),
     "spgemm_tw_f16_noalloc": (ctypes.c_int, [_p, _i64, ctypes.POINTER(SpgTwDesc), _p, _i64, _i64, _p]),
+    "layernorm": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, ctypes.c_float, _p, _i64, _p, _p, _i64, _i64,
+                                 ctypes.c_int, ctypes.c_int, _p]),
+    "layernorm_s8": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, ctypes.c_float, ctypes.c_float, _p, _i64,
+                                    _i64, _i64, ctypes.c_int, ctypes.c_int, _p]),
+    "layernorm_bwd_workspace_size": (_sz, [_i64, _i64, ctypes.c_int]),
+    "layernorm_bwd": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _sz, _i64, _i64,
+                                     ctypes.c_int, ctypes.c_int, _p]),
 }
 
 _lib = None
@@ -474,3 +481,157 @@ def spgemm_tw_f16_noalloc(X, desc: TwDesc, Y=None, stream=None):
     _check("spgemm_tw_f16_noalloc", lib().spgemm_tw_f16_noalloc(
         _ptr(X), X.stride(0), ctypes.byref(desc.c), _ptr(Y), Y.stride(0), M, _stream(stream)))
     return Y
+
+
+def _float_code(t, name: str, dtypes) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    return {torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32}[t.dtype]
+
+
+def _like(t, name: str, dtype, shape, dev: int, contiguous=False, optional=False):
+    """_arg for the further tensors of a call whose first one passed it: one dtype,
+    the exact shape and the first tensor's device (``dev``), with the checks in the
+    order that costs a valid call least."""
+    import torch
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
+            not (t.is_contiguous() or (not contiguous and len(shape) == 2)):
+        _arg(t, name, (dtype,), shape, contiguous=contiguous or len(shape) != 2)
+        raise ValueError(f"{name} is on {t.device}, the other arguments are on device {dev}")
+    if len(shape) == 2 and shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major with unit column stride (got strides {t.stride()})")
+    return t
+
+
+def _pitch(t) -> int:
+    """Row pitch in elements; a single row has none of its own, so it takes the next multiple of 8."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _new(shape, dtype, device, stream, pad=False):
+    """A tensor the call writes.  One that is used on another stream than the current
+    one is taken from that stream's memory, so that neither its memory's last use nor
+    its next one can overlap the call.  ``pad``: rows padded to 16 bytes."""
+    import torch
+    if stream is not None and device.type == "cuda":
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(
+            getattr(stream, "cuda_stream", stream)), device=device)
+        with torch.cuda.stream(s):
+            return _new(shape, dtype, device, None, pad)
+    if pad and (shape[1] * dtype.itemsize) % 16:
+        step = 16 // dtype.itemsize
+        return torch.empty((shape[0], (shape[1] + step - 1) // step * step), dtype=dtype, device=device)[:, :shape[1]]
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _apart(outs) -> None:
+    """The call's outputs do not share memory: each byte is written for one of them."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + ((t.shape[0] - 1) * _pitch(t) + t.shape[1]) * t.element_size()
+                    if t.dim() == 2 else t.data_ptr() + t.numel() * t.element_size(), n)
+                   for n, t in outs if t is not None and t.numel())
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"{a} and {b} share memory")
+
+
+def _ln_args(X, gamma, beta, residual, H):
+    import torch
+    code = _float_code(X, "X", (torch.float16, torch.bfloat16, torch.float32))
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, C = X.shape
+    _arg(X, "X", (X.dtype,))
+    dev = X.get_device()
+    wcode = _float_code(gamma, "gamma", (X.dtype, torch.float32))
+    _like(gamma, "gamma", gamma.dtype, (C,), dev, contiguous=True)
+    _like(beta, "beta", gamma.dtype, (C,), dev, contiguous=True, optional=True)
+    _like(residual, "residual", X.dtype, (M, C), dev, optional=True)
+    if residual is None and H is not None:
+        raise ValueError("H is the sum of X and residual: it needs a residual")
+    _like(H, "H", X.dtype, (M, C), dev, optional=True)
+    return M, C, dev, code, wcode
+
+
+def layernorm(X, gamma, beta=None, eps=1e-5, residual=None, H=None, Y=None, stats=False, stream=None):
+    """Layer norm of X [M, C] (or of H = X + residual), fp16, bf16 or fp32; gamma and
+    beta [C] in X's dtype or fp32.  Returns (Y, H, mean, rstd): H is None without a
+    residual, mean and rstd (fp32 [M], for layernorm_bwd) are None without ``stats``."""
+    import torch
+    M, C, dev, code, wcode = _ln_args(X, gamma, beta, residual, H)
+    if residual is not None and H is None:
+        H = _new((M, C), X.dtype, X.device, stream, pad=True)
+    if Y is None:
+        Y = _new((M, C), X.dtype, X.device, stream, pad=True)
+    else:
+        _like(Y, "Y", X.dtype, (M, C), dev)
+        _apart((("Y", Y), ("H", H)))
+    st = _new((2, M), torch.float32, X.device, stream) if stats else None
+    mean, rstd = (st[0], st[1]) if stats else (None, None)
+    _check("layernorm", lib().layernorm(
+        _ptr(X), _pitch(X), _ptr(residual), _pitch(residual), _ptr(H), _pitch(H), _ptr(gamma), _ptr(beta), eps,
+        _ptr(Y), _pitch(Y), _ptr(mean), _ptr(rstd), M, C, code, wcode, _stream(stream)))
+    return Y, H, mean, rstd
+
+
+def layernorm_s8(X, gamma, beta, qscale, eps=1e-5, residual=None, H=None, Yq=None, stream=None):
+    """Layer norm of X [M, C] (or of H = X + residual) quantised to the int8 activations of
+    an int8 2:4 layer: Yq = clamp(rne(y * qscale), -127, 127).  Returns (Yq, H)."""
+    import torch
+    M, C, dev, code, wcode = _ln_args(X, gamma, beta, residual, H)
+    if residual is not None and H is None:
+        H = _new((M, C), X.dtype, X.device, stream, pad=True)
+    if Yq is None:
+        Yq = _new((M, C), torch.int8, X.device, stream, pad=True)
+    else:
+        _like(Yq, "Yq", torch.int8, (M, C), dev)
+        _apart((("Yq", Yq), ("H", H)))
+    _check("layernorm_s8", lib().layernorm_s8(
+        _ptr(X), _pitch(X), _ptr(residual), _pitch(residual), _ptr(H), _pitch(H), _ptr(gamma), _ptr(beta), eps,
+        qscale, _ptr(Yq), _pitch(Yq) if M > 1 else (C + 15) // 16 * 16, M, C, code, wcode, _stream(stream)))
+    return Yq, H
+
+
+def layernorm_bwd(dY, X, mean, rstd, gamma, dH=None, dX=None, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """Gradients of layernorm: X is what the norm was taken of (H where there was a
+    residual), dH [M, C] the gradient that reaches it by the residual path.  Returns
+    (dX, dgamma, dbeta), the last two in gamma's dtype."""
+    import torch
+    M, C, dev, code, wcode = _ln_args(X, gamma, None, None, None)
+    _like(dY, "dY", X.dtype, (M, C), dev)
+    _like(dH, "dH", X.dtype, (M, C), dev, optional=True)
+    _like(mean, "mean", torch.float32, (M,), dev, contiguous=True)
+    _like(rstd, "rstd", torch.float32, (M,), dev, contiguous=True)
+    mine = dX is None and dgamma is None and dbeta is None
+    if dX is None:
+        dX = _new((M, C), X.dtype, X.device, stream, pad=True)
+    if dgamma is None:
+        dgamma = _new((C,), gamma.dtype, X.device, stream)
+    if dbeta is None:
+        dbeta = _new((C,), gamma.dtype, X.device, stream)
+    need = int(lib().layernorm_bwd_workspace_size(M, C, code))
+    if workspace is None:
+        workspace = _new((need,), torch.uint8, X.device, stream)
+    else:
+        workspace = _workspace(workspace, need, X.device)
+        mine = False
+    if not mine:
+        _like(dX, "dX", X.dtype, (M, C), dev)
+        _like(dgamma, "dgamma", gamma.dtype, (C,), dev, contiguous=True)
+        _like(dbeta, "dbeta", gamma.dtype, (C,), dev, contiguous=True)
+        _apart((("dX", dX), ("dgamma", dgamma), ("dbeta", dbeta), ("workspace", workspace)))
+    _check("layernorm_bwd", lib().layernorm_bwd(
+        _ptr(dY), _pitch(dY), _ptr(X), _pitch(X), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dH), _pitch(dH), _ptr(dX),
+        _pitch(dX), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace), M, C, code, wcode,
+        _stream(stream)))
+    return dX, dgamma, dbeta
