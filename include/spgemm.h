@@ -438,6 +438,65 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
                          void* dgamma, void* dbeta, void* workspace, size_t ws_bytes, int64_t M, int64_t C,
                          spg_dtype dtype, spg_dtype wdtype, spg_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * lora_plan, lora_f16, lora_f16_bwd  (no counterpart on the pages: low-rank
+ * adapters beside a frozen pruned layer, for serving many fine-tuned variants
+ * of one model in one batch and for fine-tuning it)
+ *
+ * Row m of the batch uses adapter l = index[m], or none.  A_l is [R, K], B_l
+ * [N, R], s_l = scale[l].
+ *   lora_f16:      V[m] = round(x A_l^T)
+ *                  Y[m] = round(base[m] + s_l V[m] B_l^T)
+ *   lora_f16_bwd:  U[m] = round(s_l dY[m] B_l)
+ *                  dX[m] = round(dbase[m] + U[m] A_l)
+ *                  dA_l = round(sum over l's rows of U[m]^T x)
+ *                  dB_l = round(s_l sum over l's rows of dY[m]^T V[m])
+ * Products are summed in fp32; round() is one round-to-nearest-even to `dtype`
+ * (SPG_F16 or SPG_BF16, the type of every matrix).  Rows without an adapter
+ * get V = 0, Y = base and dX = dbase and take no part in the gradients; an
+ * adapter without rows gets gradients of +0.  Results do not depend on timing,
+ * nor does a row's or an adapter's result on what other rows or adapters hold.
+ *
+ * lora_plan groups the rows by adapter on the device, for all calls on this
+ * batch and these L adapters (every layer of the model, forward and backward):
+ *   index int32 [M], device; values outside [0, L) mean no adapter
+ *   plan  int32, device, 16-byte aligned, plan_bytes >= lora_plan_size(M, L);
+ *         opaque, only read by the calls below, which must be given the same
+ *         M and L.  It may be refilled for a new index of the same M and L
+ *         (a captured graph then follows it).
+ * Arguments of the calls:
+ *   X     [M, K], pitch ldx;  dY [M, N], pitch lddy
+ *   A     [L, R, K] and B [L, N, R], contiguous; scale fp32 [L] or NULL (1)
+ *   V     [M, R], pitch ldv: written by lora_f16, read by lora_f16_bwd
+ *   base  [M, N], pitch ldbase, or NULL (0); Y [M, N], pitch ldy, may be the
+ *         same memory as base (same pointer and pitch): the shared layer's
+ *         output with the adapters added in place
+ *   dbase [M, K], pitch lddbase, or NULL (0): the shared layer's gradient of X;
+ *   dX    [M, K], pitch lddx, may be the same memory as dbase; NULL: not needed
+ *   dA    [L, R, K], dB [L, N, R], contiguous, written whole
+ *   workspace 16-byte aligned, ws_bytes >= lora_bwd_workspace_size; scratch,
+ *         calls that may overlap need one each
+ * Limits: K % 8 == 0, R % 8 == 0, R <= 128, 1 <= L <= 8192, M < 2^22; N >= 1
+ * (any).  X, V, base, Y, dY, dbase, dX 16-byte aligned with pitches that are
+ * multiples of 8; A, B, dA, dB, plan 16-byte aligned.  M == 0 is valid:
+ * lora_f16 does nothing, lora_f16_bwd writes zeros to dA and dB.
+ * ------------------------------------------------------------------------- */
+size_t lora_plan_size(int64_t M, int64_t L); /* bytes; 0 for sizes outside the limits */
+
+spg_status lora_plan(const int32_t* index, int64_t M, int64_t L, int32_t* plan, size_t plan_bytes,
+                     spg_stream_t stream);
+
+spg_status lora_f16(const void* X, int64_t ldx, const void* A, const void* B, const float* scale, const int32_t* plan,
+                    void* V, int64_t ldv, const void* base, int64_t ldbase, void* Y, int64_t ldy, int64_t M, int64_t N,
+                    int64_t K, int64_t R, int64_t L, spg_dtype dtype, spg_stream_t stream);
+
+size_t lora_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L);
+
+spg_status lora_f16_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* V, int64_t ldv,
+                        const void* A, const void* B, const float* scale, const int32_t* plan, const void* dbase,
+                        int64_t lddbase, void* dX, int64_t lddx, void* dA, void* dB, void* workspace, size_t ws_bytes,
+                        int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, spg_dtype dtype, spg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -69,6 +69,13 @@ SIGNATURES = {
     "spgemm_tw_f32": (ctypes.c_int, [_p, _i64, ctypes.c_int, ctypes.POINTER(SpgTwDesc), _p, _p, _i64, _i64, _p, _sz,
                                      _p]),
     "spgemm_tw_f16_noalloc": (ctypes.c_int, [_p, _i64, ctypes.POINTER(SpgTwDesc), _p, _i64, _i64, _p]),
+    "lora_plan_size": (_sz, [_i64, _i64]),
+    "lora_plan": (ctypes.c_int, [_p, _i64, _i64, _p, _sz, _p]),
+    "lora_f16": (ctypes.c_int, [_p, _i64, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i64,
+                                ctypes.c_int, _p]),
+    "lora_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "lora_f16_bwd": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _sz,
+                                    _i64, _i64, _i64, _i64, _i64, ctypes.c_int, _p]),
     "layernorm": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, ctypes.c_float, _p, _i64, _p, _p, _i64, _i64,
                                  ctypes.c_int, ctypes.c_int, _p]),
     "layernorm_s8": (ctypes.c_int, [_p, _i64, _p, _i64, _p, _i64, _p, _p, ctypes.c_float, ctypes.c_float, _p, _i64,
@@ -483,155 +490,279 @@ def spgemm_tw_f16_noalloc(X, desc: TwDesc, Y=None, stream=None):
     return Y
 
 
-def _float_code(t, name: str, dtypes) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    return {torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32}[t.dtype]
+_torch = None
+_FLOAT_CODES: dict = {}
 
 
-def _like(t, name: str, dtype, shape, dev: int, contiguous=False, optional=False):
-    """_arg for the further tensors of a call whose first one passed it: one dtype,
-    the exact shape and the first tensor's device (``dev``), with the checks in the
-    order that costs a valid call least."""
-    import torch
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
-            not (t.is_contiguous() or (not contiguous and len(shape) == 2)):
-        _arg(t, name, (dtype,), shape, contiguous=contiguous or len(shape) != 2)
-        raise ValueError(f"{name} is on {t.device}, the other arguments are on device {dev}")
-    if len(shape) == 2 and shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be row-major with unit column stride (got strides {t.stride()})")
-    return t
+def _tm():
+    """torch, imported with the first call that needs it (the package itself also builds without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _FLOAT_CODES.update({torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32})
+        _torch = torch
+    return _torch
 
 
-def _pitch(t) -> int:
-    """Row pitch in elements; a single row has none of its own, so it takes the next multiple of 8."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+def _like(t, name: str, dtype, shape, dev: int) -> int:
+    """_arg for the further tensors of a call whose first one passed it (its device is
+    ``dev``): a valid tensor costs a few comparisons, any other one gets _arg's message.
+    Matrices may have a row pitch, which is returned; others are contiguous."""
+    if t.__class__ is _torch.Tensor or isinstance(t, _torch.Tensor):
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            if len(shape) == 2:
+                ld, unit = t.stride()
+                if unit == 1 or shape[1] <= 1 or not shape[0]:
+                    # a single row has no pitch of its own: the next multiple of 16
+                    return ld if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+            elif t.is_contiguous():
+                return 0
+    _arg(t, name, (dtype,), shape, contiguous=len(shape) != 2)
+    raise ValueError(f"{name} is on {t.device}, the other arguments are on device {dev}")
 
 
-def _new(shape, dtype, device, stream, pad=False):
-    """A tensor the call writes.  One that is used on another stream than the current
-    one is taken from that stream's memory, so that neither its memory's last use nor
-    its next one can overlap the call.  ``pad``: rows padded to 16 bytes."""
-    import torch
-    if stream is not None and device.type == "cuda":
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(
-            getattr(stream, "cuda_stream", stream)), device=device)
-        with torch.cuda.stream(s):
-            return _new(shape, dtype, device, None, pad)
-    if pad and (shape[1] * dtype.itemsize) % 16:
+def _first(t, name: str, dtypes, dims: int = 2) -> int:
+    """_arg for a call's first tensor; returns its row pitch."""
+    _arg(t, name, dtypes)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D")
+    return _like(t, name, t.dtype, t.shape, t.get_device())
+
+
+def _on_stream(stream, device):
+    """The stream as a torch stream (a raw handle is wrapped)."""
+    torch = _tm()
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
+def _new(shape, dtype, like, stream, pad=False):
+    """A tensor that the call writes, on the device of ``like``.  Where the call goes to
+    another stream than the current one, the memory is that stream's, so that neither its
+    last use nor its next one can overlap the call.  ``pad``: rows padded to 16 bytes."""
+    if stream is not None and like.is_cuda:
+        with _torch.cuda.stream(_on_stream(stream, like.device)):
+            return _new(shape, dtype, like, None, pad)
+    if pad:
+        M, C = shape
         step = 16 // dtype.itemsize
-        return torch.empty((shape[0], (shape[1] + step - 1) // step * step), dtype=dtype, device=device)[:, :shape[1]]
-    return torch.empty(shape, dtype=dtype, device=device)
+        if C % step:
+            return like.new_empty((M, (C + step - 1) // step * step), dtype=dtype)[:, :C]
+    return like.new_empty(shape, dtype=dtype)
 
 
-def _apart(outs) -> None:
+def _apart(**outs) -> None:
     """The call's outputs do not share memory: each byte is written for one of them."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + ((t.shape[0] - 1) * _pitch(t) + t.shape[1]) * t.element_size()
-                    if t.dim() == 2 else t.data_ptr() + t.numel() * t.element_size(), n)
-                   for n, t in outs if t is not None and t.numel())
+    spans = []
+    for name, t in outs.items():
+        if t is not None and t.numel():
+            n = (t.shape[0] - 1) * t.stride(0) + t.shape[1] if t.dim() == 2 else t.numel()
+            spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(), name))
+    spans.sort()
     for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
         if start < end:
             raise ValueError(f"{a} and {b} share memory")
 
 
-def _ln_args(X, gamma, beta, residual, H):
-    import torch
-    code = _float_code(X, "X", (torch.float16, torch.bfloat16, torch.float32))
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
-    M, C = X.shape
-    _arg(X, "X", (X.dtype,))
+def _ln_args(X, gamma):
+    """X [M, C] and gamma [C] of the layer norm calls; returns X's pitch and device index and the type codes."""
+    torch = _tm()
+    ldx = _first(X, "X", (torch.float16, torch.bfloat16, torch.float32))
     dev = X.get_device()
-    wcode = _float_code(gamma, "gamma", (X.dtype, torch.float32))
-    _like(gamma, "gamma", gamma.dtype, (C,), dev, contiguous=True)
-    _like(beta, "beta", gamma.dtype, (C,), dev, contiguous=True, optional=True)
-    _like(residual, "residual", X.dtype, (M, C), dev, optional=True)
-    if residual is None and H is not None:
+    wdt = torch.float32 if getattr(gamma, "dtype", None) is torch.float32 else X.dtype
+    _like(gamma, "gamma", wdt, X.shape[1:], dev)
+    return ldx, dev, _FLOAT_CODES[X.dtype], _FLOAT_CODES[wdt]
+
+
+def _ln_fwd(fn, X, gamma, beta, eps, qscale, residual, H, Y, ydt, stats, stream):
+    ldx, dev, code, wcode = _ln_args(X, gamma)
+    shape, dt = X.shape, X.dtype
+    M, C = shape
+    if beta is not None:
+        _like(beta, "beta", gamma.dtype, gamma.shape, dev)
+    res = h = None
+    ldres = ldh = 0
+    if residual is not None:
+        ldres = _like(residual, "residual", dt, shape, dev)
+        res = residual.data_ptr()
+        if H is None:
+            H = _new(shape, dt, X, stream, pad=True)
+        ldh = _like(H, "H", dt, shape, dev)
+        h = H.data_ptr()
+    elif H is not None:
         raise ValueError("H is the sum of X and residual: it needs a residual")
-    _like(H, "H", X.dtype, (M, C), dev, optional=True)
-    return M, C, dev, code, wcode
+    if Y is None:
+        Y = _new(shape, ydt, X, stream, pad=True)
+        ldy = _like(Y, "Y", ydt, shape, dev)
+    else:
+        ldy = _like(Y, "Y", ydt, shape, dev)
+        _apart(Y=Y, H=H)
+    if qscale is None:
+        mean = rstd = None
+        if stats:
+            mean, rstd = _new((2, M), _torch.float32, X, stream).unbind()
+        _check(fn, lib().layernorm(
+            X.data_ptr(), ldx, res, ldres, h, ldh, gamma.data_ptr(), _ptr(beta), eps, Y.data_ptr(), ldy, _ptr(mean),
+            _ptr(rstd), M, C, code, wcode, _stream(stream)))
+        return Y, H, mean, rstd
+    _check(fn, lib().layernorm_s8(
+        X.data_ptr(), ldx, res, ldres, h, ldh, gamma.data_ptr(), _ptr(beta), eps, qscale, Y.data_ptr(), ldy, M, C,
+        code, wcode, _stream(stream)))
+    return Y, H
 
 
 def layernorm(X, gamma, beta=None, eps=1e-5, residual=None, H=None, Y=None, stats=False, stream=None):
     """Layer norm of X [M, C] (or of H = X + residual), fp16, bf16 or fp32; gamma and
     beta [C] in X's dtype or fp32.  Returns (Y, H, mean, rstd): H is None without a
     residual, mean and rstd (fp32 [M], for layernorm_bwd) are None without ``stats``."""
-    import torch
-    M, C, dev, code, wcode = _ln_args(X, gamma, beta, residual, H)
-    if residual is not None and H is None:
-        H = _new((M, C), X.dtype, X.device, stream, pad=True)
-    if Y is None:
-        Y = _new((M, C), X.dtype, X.device, stream, pad=True)
-    else:
-        _like(Y, "Y", X.dtype, (M, C), dev)
-        _apart((("Y", Y), ("H", H)))
-    st = _new((2, M), torch.float32, X.device, stream) if stats else None
-    mean, rstd = (st[0], st[1]) if stats else (None, None)
-    _check("layernorm", lib().layernorm(
-        _ptr(X), _pitch(X), _ptr(residual), _pitch(residual), _ptr(H), _pitch(H), _ptr(gamma), _ptr(beta), eps,
-        _ptr(Y), _pitch(Y), _ptr(mean), _ptr(rstd), M, C, code, wcode, _stream(stream)))
-    return Y, H, mean, rstd
+    return _ln_fwd("layernorm", X, gamma, beta, eps, None, residual, H, Y, getattr(X, "dtype", None), stats, stream)
 
 
 def layernorm_s8(X, gamma, beta, qscale, eps=1e-5, residual=None, H=None, Yq=None, stream=None):
     """Layer norm of X [M, C] (or of H = X + residual) quantised to the int8 activations of
     an int8 2:4 layer: Yq = clamp(rne(y * qscale), -127, 127).  Returns (Yq, H)."""
-    import torch
-    M, C, dev, code, wcode = _ln_args(X, gamma, beta, residual, H)
-    if residual is not None and H is None:
-        H = _new((M, C), X.dtype, X.device, stream, pad=True)
-    if Yq is None:
-        Yq = _new((M, C), torch.int8, X.device, stream, pad=True)
-    else:
-        _like(Yq, "Yq", torch.int8, (M, C), dev)
-        _apart((("Yq", Yq), ("H", H)))
-    _check("layernorm_s8", lib().layernorm_s8(
-        _ptr(X), _pitch(X), _ptr(residual), _pitch(residual), _ptr(H), _pitch(H), _ptr(gamma), _ptr(beta), eps,
-        qscale, _ptr(Yq), _pitch(Yq) if M > 1 else (C + 15) // 16 * 16, M, C, code, wcode, _stream(stream)))
-    return Yq, H
+    return _ln_fwd("layernorm_s8", X, gamma, beta, eps, float(qscale), residual, H, Yq, _tm().int8, False, stream)
 
 
 def layernorm_bwd(dY, X, mean, rstd, gamma, dH=None, dX=None, dgamma=None, dbeta=None, workspace=None, stream=None):
     """Gradients of layernorm: X is what the norm was taken of (H where there was a
     residual), dH [M, C] the gradient that reaches it by the residual path.  Returns
     (dX, dgamma, dbeta), the last two in gamma's dtype."""
-    import torch
-    M, C, dev, code, wcode = _ln_args(X, gamma, None, None, None)
-    _like(dY, "dY", X.dtype, (M, C), dev)
-    _like(dH, "dH", X.dtype, (M, C), dev, optional=True)
-    _like(mean, "mean", torch.float32, (M,), dev, contiguous=True)
-    _like(rstd, "rstd", torch.float32, (M,), dev, contiguous=True)
-    mine = dX is None and dgamma is None and dbeta is None
+    ldx, dev, code, wcode = _ln_args(X, gamma)
+    shape, dt, wdt = X.shape, X.dtype, gamma.dtype
+    M, C = shape
+    lddy = _like(dY, "dY", dt, shape, dev)
+    _like(mean, "mean", _torch.float32, (M,), dev)
+    _like(rstd, "rstd", _torch.float32, (M,), dev)
+    lddh = 0 if dH is None else _like(dH, "dH", dt, shape, dev)
+    given = not (dX is None and dgamma is None and dbeta is None and workspace is None)
     if dX is None:
-        dX = _new((M, C), X.dtype, X.device, stream, pad=True)
-    if dgamma is None:
-        dgamma = _new((C,), gamma.dtype, X.device, stream)
-    if dbeta is None:
-        dbeta = _new((C,), gamma.dtype, X.device, stream)
-    need = int(lib().layernorm_bwd_workspace_size(M, C, code))
+        dX = _new(shape, dt, X, stream, pad=True)
+    lddx = _like(dX, "dX", dt, shape, dev)
+    if dgamma is None and dbeta is None:
+        dgamma, dbeta = _new((2, C), wdt, X, stream).unbind()
+    dgamma = _new((C,), wdt, X, stream) if dgamma is None else dgamma
+    dbeta = _new((C,), wdt, X, stream) if dbeta is None else dbeta
+    need = lib().layernorm_bwd_workspace_size(M, C, code)
     if workspace is None:
-        workspace = _new((need,), torch.uint8, X.device, stream)
-    else:
-        workspace = _workspace(workspace, need, X.device)
-        mine = False
-    if not mine:
-        _like(dX, "dX", X.dtype, (M, C), dev)
-        _like(dgamma, "dgamma", gamma.dtype, (C,), dev, contiguous=True)
-        _like(dbeta, "dbeta", gamma.dtype, (C,), dev, contiguous=True)
-        _apart((("dX", dX), ("dgamma", dgamma), ("dbeta", dbeta), ("workspace", workspace)))
+        workspace = _new((need,), _torch.uint8, X, stream)
+    if given:
+        _workspace(workspace, need, X.device)
+        _like(dgamma, "dgamma", wdt, (C,), dev)
+        _like(dbeta, "dbeta", wdt, (C,), dev)
+        _apart(dX=dX, dgamma=dgamma, dbeta=dbeta, workspace=workspace)
     _check("layernorm_bwd", lib().layernorm_bwd(
-        _ptr(dY), _pitch(dY), _ptr(X), _pitch(X), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dH), _pitch(dH), _ptr(dX),
-        _pitch(dX), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace), M, C, code, wcode,
-        _stream(stream)))
+        dY.data_ptr(), lddy, X.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(), gamma.data_ptr(), _ptr(dH), lddh,
+        dX.data_ptr(), lddx, dgamma.data_ptr(), dbeta.data_ptr(), workspace.data_ptr(), _nbytes(workspace), M, C, code,
+        wcode, _stream(stream)))
     return dX, dgamma, dbeta
+
+
+class LoraPlan:
+    """The rows of a batch grouped by adapter (device memory filled by ``lora_plan``)."""
+
+    def __init__(self, buf, M: int, L: int):
+        self.buf, self.M, self.L = buf, M, L
+
+
+def lora_plan(index, L: int, plan: Optional[LoraPlan] = None, stream=None) -> LoraPlan:
+    """Group the rows of a batch by adapter: index int32 [M] names the adapter of each row,
+    values outside [0, L) none.  One plan serves every layer's lora_f16 and
+    lora_f16_bwd of the batch.  ``plan`` refills an earlier plan of the same M and L."""
+    torch = _tm()
+    _first(index, "index", (torch.int32,), dims=1)
+    M, L = index.shape[0], int(L)
+    need = lib().lora_plan_size(M, L)
+    if plan is None:
+        plan = LoraPlan(_new((need // 4,), torch.int32, index, stream), M, L)
+    elif plan.M != M or plan.L != L:
+        raise ValueError(f"plan is for {plan.M} rows and {plan.L} adapters, the index for {M} and {L}")
+    else:
+        _like(plan.buf, "plan", torch.int32, (need // 4,), index.get_device())
+    _check("lora_plan", lib().lora_plan(index.data_ptr(), M, L, plan.buf.data_ptr(), plan.buf.numel() * 4,
+                                        _stream(stream)))
+    return plan
+
+
+def _lora_args(X, A, B, plan, scale):
+    """What both directions share; returns X's pitch, the device index and N, K, R, L."""
+    torch = _tm()
+    ldx = _first(X, "X", (torch.float16, torch.bfloat16))
+    dev, dt = X.get_device(), X.dtype
+    if not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan (see lora_plan)")
+    L = plan.L
+    if A is None or B is None or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [L, R, K] and B [L, N, R]")
+    R, N = A.shape[1], B.shape[1]
+    M, K = X.shape
+    if M != plan.M:
+        raise ValueError(f"X has {M} rows, the plan is for {plan.M}")
+    _like(A, "A", dt, (L, R, K), dev)
+    _like(B, "B", dt, (L, N, R), dev)
+    if plan.buf.get_device() != dev:
+        raise ValueError(f"plan is on {plan.buf.device}, X on {X.device}")
+    if scale is not None:
+        _like(scale, "scale", torch.float32, (L,), dev)
+    return ldx, dev, N, K, R, L
+
+
+def lora_f16(X, A, B, plan: LoraPlan, scale=None, base=None, Y=None, V=None, stream=None):
+    """Adapters' contribution added to a shared layer's output: with l the adapter of row m,
+    V[m] = X[m] . A[l]^T and Y[m] = base[m] + scale[l] * V[m] . B[l]^T, fp16 or bf16.
+    X [M, K], A [L, R, K], B [L, N, R], scale fp32 [L] (1 without), base [M, N] (0 without;
+    Y may be base itself).  Returns (Y, V); V [M, R] is what lora_f16_bwd needs."""
+    ldx, dev, N, K, R, L = _lora_args(X, A, B, plan, scale)
+    dt, M = X.dtype, plan.M
+    ldbase = 0 if base is None else _like(base, "base", dt, (M, N), dev)
+    given = not (Y is None and V is None)
+    if V is None:
+        V = _new((M, R), dt, X, stream)
+    if Y is None:
+        Y = _new((M, N), dt, X, stream, pad=True)
+    ldv, ldy = _like(V, "V", dt, (M, R), dev), _like(Y, "Y", dt, (M, N), dev)
+    if given:
+        _apart(Y=Y, V=V)
+    _check("lora_f16", lib().lora_f16(
+        X.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), _ptr(scale), plan.buf.data_ptr(), V.data_ptr(), ldv, _ptr(base),
+        ldbase, Y.data_ptr(), ldy, M, N, K, R, L, _FLOAT_CODES[dt], _stream(stream)))
+    return Y, V
+
+
+def lora_f16_bwd(dY, X, V, A, B, plan: LoraPlan, scale=None, dbase=None, dX=None, dA=None, dB=None, workspace=None,
+                 need_dx=True, stream=None):
+    """Gradients of lora_f16: with U[m] = scale[l] * dY[m] . B[l], dX[m] = dbase[m] + U[m] . A[l]
+    (dbase [M, K]: the shared layer's gradient of X, 0 without; dX may be dbase itself),
+    dA[l] the sum of U[m]^T X[m] and dB[l] of scale[l] * dY[m]^T V[m] over l's rows.
+    Returns (dX, dA, dB); dX is None with ``need_dx=False``."""
+    ldx, dev, N, K, R, L = _lora_args(X, A, B, plan, scale)
+    dt, M = X.dtype, plan.M
+    lddy = _like(dY, "dY", dt, (M, N), dev)
+    ldv = _like(V, "V", dt, (M, R), dev)
+    lddb = 0 if dbase is None else _like(dbase, "dbase", dt, (M, K), dev)
+    given = not (dX is None and dA is None and dB is None and workspace is None)
+    if not need_dx and (dX is not None or dbase is not None):
+        raise ValueError("need_dx=False takes neither dX nor dbase")
+    lddx = 0
+    if need_dx:
+        if dX is None:
+            dX = _new((M, K), dt, X, stream)
+        lddx = _like(dX, "dX", dt, (M, K), dev)
+    if dA is None:
+        dA = _new((L, R, K), dt, X, stream)
+    if dB is None:
+        dB = _new((L, N, R), dt, X, stream)
+    need = lib().lora_bwd_workspace_size(M, N, K, R, L)
+    if workspace is None:
+        workspace = _new((need,), _torch.uint8, X, stream)
+    if given:
+        _like(dA, "dA", dt, (L, R, K), dev)
+        _like(dB, "dB", dt, (L, N, R), dev)
+        _workspace(workspace, need, X.device)
+        _apart(dX=dX, dA=dA, dB=dB, workspace=workspace)
+    _check("lora_f16_bwd", lib().lora_f16_bwd(
+        dY.data_ptr(), lddy, X.data_ptr(), ldx, V.data_ptr(), ldv, A.data_ptr(), B.data_ptr(), _ptr(scale),
+        plan.buf.data_ptr(), _ptr(dbase), lddb, _ptr(dX), lddx, dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(),
+        _nbytes(workspace), M, N, K, R, L, _FLOAT_CODES[dt], _stream(stream)))
+    return dX, dA, dB
