@@ -17,7 +17,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
+#include "gather.cuh"
 #include "host.cuh"
 #include "sm100.cuh"
 #include "spgemm.h"
@@ -25,37 +27,33 @@
 namespace spg {
 namespace norm {
 
-// One 16-byte vector of a row: VE elements of T as they lie in memory.
-template <class T>
-struct Vec {
-  static constexpr int VE = 16 / sizeof(T);
-  union {
-    uint4 raw;
-    T e[VE];
-  };
-  __device__ Vec() : raw(make_uint4(0u, 0u, 0u, 0u)) {}
-  // elements [0, n) from p; a whole vector in one load where AL says that p is 16-byte aligned
-  template <bool AL>
-  __device__ __forceinline__ void load(const T* p, int n) {
-    if (AL && n >= VE) {
-      raw = *reinterpret_cast<const uint4*>(p);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (i < n) e[i] = p[i];
-    }
-  }
-  template <bool AL>
-  __device__ __forceinline__ void store(T* p, int n) const {
-    if (AL && n >= VE) {
-      *reinterpret_cast<uint4*>(p) = raw;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (i < n) p[i] = e[i];
-    }
-  }
-};
+// ---- pairs of fp32 values, which the FMA pipe takes two at a time ----------------------
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_of(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -69,14 +67,111 @@ __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// VE elements of gamma or beta, in the activations' type or in fp32; 0 where the pointer is null.
+// 16 bytes of a row as they lie in memory, and as pairs of fp32 values.
 template <class T>
-__device__ __forceinline__ void load_weight(float (&w)[Vec<T>::VE], const void* p, int f32, int c, int n) {
+struct Vec {
+  static constexpr int VE = 16 / sizeof(T), VP = VE / 2;
+  uint4 raw;
+  __device__ Vec() : raw(make_uint4(0u, 0u, 0u, 0u)) {}
+  __device__ __forceinline__ void get(f2 (&v)[VP]) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (sizeof(T) == 4) {
+      v[0] = f2_of(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      v[1] = f2_of(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-  for (int i = 0; i < Vec<T>::VE; ++i)
-    w[i] = (p == nullptr || i >= n) ? 0.f
-           : f32                    ? static_cast<const float*>(p)[c + i]
-                                    : to_f(static_cast<const T*>(p)[c + i]);
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          v[k] = f2_of(f.x, f.y);
+        } else {
+          v[k] = f2_of(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const f2 (&v)[VP]) {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 4) {
+      const float2 a = f2_get(v[0]), b = f2_get(v[1]);
+      w[0] = __float_as_uint(a.x); w[1] = __float_as_uint(a.y);
+      w[2] = __float_as_uint(b.x); w[3] = __float_as_uint(b.y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = f2_get(v[k]);
+        if constexpr (std::is_same<T, __half>::value)
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(f.y), "f"(f.x));
+        else
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(f.y), "f"(f.x));
+      }
+    }
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// VE elements at p, of which the first n are inside the row.  WHOLE: all of
+// them are, and p is 16-byte aligned; otherwise they move one by one and the
+// others are 0.
+template <bool WHOLE, class T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
+  Vec<T> v;
+  if constexpr (WHOLE) {
+    v.raw = *reinterpret_cast<const uint4*>(p);
+  } else {
+    f2 f[Vec<T>::VP];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::VP; ++i)
+      f[i] = f2_of(2 * i < n ? to_f(p[2 * i]) : 0.f, 2 * i + 1 < n ? to_f(p[2 * i + 1]) : 0.f);
+    v.set(f);
+  }
+  return v;
+}
+template <bool WHOLE, class T>
+__device__ __forceinline__ void store_vec(T* p, const f2 (&f)[Vec<T>::VP], int n) {
+  if constexpr (WHOLE) {
+    Vec<T> v;
+    v.set(f);
+    *reinterpret_cast<uint4*>(p) = v.raw;
+  } else {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::VP; ++i) {
+      const float2 e = f2_get(f[i]);
+      if (2 * i < n) p[2 * i] = from_f<T>(e.x);
+      if (2 * i + 1 < n) p[2 * i + 1] = from_f<T>(e.y);
+    }
+  }
+}
+
+// VE elements of gamma or beta, in the activations' type or in fp32; 0 where the pointer is null.
+template <bool WHOLE, class T>
+__device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int f32, int c, int n) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int i = 0; i < Vec<T>::VP; ++i) w[i] = 0ull;
+  } else if (f32 || sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < Vec<T>::VP; k += 2) {
+      f2 q[2];
+      load_vec<WHOLE>(static_cast<const float*>(p) + c + 2 * k, n - 2 * k).get(q);
+      w[k] = q[0];
+      w[k + 1] = q[1];
+    }
+  } else {
+    load_vec<WHOLE>(static_cast<const T*>(p) + c, n).get(w);
+  }
+}
+
+// 0 for the elements of a vector past its row's end.
+template <bool WHOLE, int VP>
+__device__ __forceinline__ void clear_past(f2 (&v)[VP], int n) {
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const float2 e = f2_get(v[i]);
+      v[i] = f2_of(2 * i < n ? e.x : 0.f, 2 * i + 1 < n ? e.y : 0.f);
+    }
+  }
 }
 
 // Threads of the largest block: 16384 columns are 2048 vectors of a 16-bit type
@@ -84,34 +179,30 @@ __device__ __forceinline__ void load_weight(float (&w)[Vec<T>::VE], const void* 
 template <class T, int NV>
 constexpr int max_threads() { return sizeof(T) == 4 && NV == 4 ? 1024 : 512; }
 
-// Sums over the threads of a row: `tpr` lanes of a warp (a power of two), or
-// the whole block through shared memory.  The two halves of `red` alternate,
-// so one barrier a reduction is enough.
-struct RowSum {
-  float2* red;  // 2 x 32
-  int tpr;      // 0: the block
-  int turn;
-  __device__ float2 operator()(float2 v) {
-    const int width = tpr ? tpr : 32;
-    for (int o = width >> 1; o; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if (tpr) return v;
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    float2* r = red + 32 * turn;
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = r[0];
-    for (int w = 1; w < warps; ++w) {
-      v.x += r[w].x;
-      v.y += r[w].y;
-    }
-    return v;
+// Sum over the 2^lg lanes of a warp that share a row.
+__device__ __forceinline__ float lanes_sum(float v, int lg) {
+  for (int o = (1 << lg) >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over the block through `red` (one float a warp, up to a multiple of
+// four, the unused ones 0); the caller alternates between two such arrays, so
+// one barrier a sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float4 s = *reinterpret_cast<const float4*>(red);
+  for (int w = 4; w < int(blockDim.x >> 5); w += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(red + w);
+    s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
   }
-};
+  return (s.x + s.y) + (s.z + s.w);
+}
 
 struct FwdArgs {
   const void* x;
@@ -122,86 +213,110 @@ struct FwdArgs {
   const void* beta;
   float* mean;
   float* rstd;
-  int64_t ldx, ldres, ldh, ldy, M;
-  int C, tpr, wf32, s8;
+  int64_t ldx, ldres, ldh, ldy;
+  int M, C, lg, wf32, s8;
   float eps, qscale;
 };
 
-// A row belongs to `tpr` lanes of a warp (tpr > 0) or to the block (tpr = 0);
+// LANES: a row belongs to 2^lg lanes of a warp, otherwise to the block;
 // thread t of the row holds vectors t, t + threads, ... (NV of them).
-template <class T, int NV, bool AL>
+// WHOLE: C is a multiple of the vector and every row 16-byte aligned.
+template <class T, int NV, bool WHOLE, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdArgs a) {
-  constexpr int VE = Vec<T>::VE;
-  __shared__ float2 red[64];
-  const int threads = a.tpr ? a.tpr : blockDim.x;
-  const int t = threadIdx.x % threads;
-  const int64_t row0 = a.tpr ? int64_t(blockIdx.x) * (blockDim.x / threads) + threadIdx.x / threads : blockIdx.x;
-  const bool live = row0 < a.M;
-  const int64_t row = live ? row0 : a.M - 1;  // lanes past the last row follow it and write nothing
+  constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
+  __shared__ __align__(16) float red[LANES ? 4 : 64];
+  const int threads = LANES ? 1 << a.lg : blockDim.x;
+  const int t = LANES ? threadIdx.x & (threads - 1) : threadIdx.x;
+  int row = blockIdx.x;
+  bool live = true;
+  if constexpr (LANES) {
+    row = (blockIdx.x * blockDim.x + threadIdx.x) >> a.lg;
+    live = row < a.M;
+    row = live ? row : a.M - 1;  // lanes past the last row follow it and write nothing
+  } else {
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.f;
+  }
   griddep_launch_dependents();
   griddep_wait();
-  RowSum sum{red, a.tpr, 0};
-  float v[NV][VE];
-  float s = 0.f;
+  f2 v[NV][VP];
+  {
+    const T* x = static_cast<const T*>(a.x) + int64_t(row) * a.ldx;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (t + k * threads) * VE;
-    const int n = a.C - c;
-    Vec<T> x;
-    if (n > 0) {
-      x.template load<AL>(static_cast<const T*>(a.x) + row * a.ldx + c, n);
-      if (a.res) {
-        Vec<T> r;
-        r.template load<AL>(static_cast<const T*>(a.res) + row * a.ldres + c, n);
-        // the backward pass reads h as it is stored, so the norm is taken of the rounded sum
-#pragma unroll
-        for (int i = 0; i < VE; ++i) x.e[i] = from_f<T>(to_f(x.e[i]) + to_f(r.e[i]));
-        if (live) x.template store<AL>(static_cast<T*>(a.h) + row * a.ldh + c, n);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      v[k][i] = to_f(x.e[i]);
-      s += v[k][i];
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * threads) * VE;
+      Vec<T> e;
+      if (c < a.C) e = load_vec<WHOLE>(x + c, a.C - c);
+      e.get(v[k]);
     }
   }
+  if constexpr (!LANES) __syncthreads();
+  if (a.res) {
+    const T* res = static_cast<const T*>(a.res) + int64_t(row) * a.ldres;
+    T* h = static_cast<T*>(a.h) + int64_t(row) * a.ldh;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * threads) * VE;
+      if (c >= a.C) continue;
+      f2 r[VP];
+      load_vec<WHOLE>(res + c, a.C - c).get(r);
+      // the backward pass reads h as it is stored, so the norm is taken of the rounded sum
+      Vec<T> e;
+#pragma unroll
+      for (int i = 0; i < VP; ++i) v[k][i] = f2_add(v[k][i], r[i]);
+      e.set(v[k]);
+      e.get(v[k]);
+      if (live) store_vec<WHOLE>(h + c, v[k], a.C - c);
+    }
+  }
+  f2 s = 0ull;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < VP; ++i) s = f2_add(s, v[k][i]);
   const float inv = 1.f / static_cast<float>(a.C);
-  const float mu = sum(make_float2(s, 0.f)).x * inv;
-  float q = 0.f;
+  float one = f2_get(s).x + f2_get(s).y;
+  const float mu = (LANES ? lanes_sum(one, a.lg) : block_sum(one, red)) * inv;
+  const f2 nmu = f2_of(-mu, -mu);
+  s = 0ull;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int n = a.C - (t + k * threads) * VE;
+    if (n <= 0) continue;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      v[k][i] -= mu;
-      q += i < n ? v[k][i] * v[k][i] : 0.f;
-    }
+    for (int i = 0; i < VP; ++i) v[k][i] = f2_add(v[k][i], nmu);
+    clear_past<WHOLE>(v[k], n);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) s = f2_fma(v[k][i], v[k][i], s);
   }
-  const float rstd = rsqrtf(sum(make_float2(q, 0.f)).x * inv + a.eps);
+  one = f2_get(s).x + f2_get(s).y;
+  const float rstd = rsqrtf((LANES ? lanes_sum(one, a.lg) : block_sum(one, red + 32)) * inv + a.eps);
   if (!live) return;
   if (t == 0) {
     if (a.mean) a.mean[row] = mu;
     if (a.rstd) a.rstd[row] = rstd;
   }
+  const f2 r2 = f2_of(rstd, rstd);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (t + k * threads) * VE;
     const int n = a.C - c;
     if (n <= 0) continue;
-    float g[VE], b[VE];
-    load_weight<T>(g, a.gamma, a.wf32, c, n);
-    load_weight<T>(b, a.beta, a.wf32, c, n);
+    f2 g[VP], b[VP];
+    load_weight<WHOLE, T>(g, a.gamma, a.wf32, c, n);
+    load_weight<WHOLE, T>(b, a.beta, a.wf32, c, n);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) v[k][i] = f2_fma(f2_mul(v[k][i], r2), g[i], b[i]);
     if (a.s8) {
       // clamp(rne(y qscale)); a NaN gives code 0
       uint32_t w[VE / 4];
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        const float y = fmaf(v[k][i] * rstd, g[i], b[i]) * a.qscale;
-        const int code = max(-127, min(127, __float2int_rn(y)));
+        const float2 e = f2_get(v[k][i / 2]);
+        const int code = max(-127, min(127, __float2int_rn((i & 1 ? e.y : e.x) * a.qscale)));
         w[i / 4] = (i % 4 ? w[i / 4] : 0u) | (static_cast<uint32_t>(code & 0xFF) << (8 * (i % 4)));
       }
-      int8_t* o = static_cast<int8_t*>(a.y) + row * a.ldy + c;
-      if (AL && n >= VE) {
+      int8_t* o = static_cast<int8_t*>(a.y) + int64_t(row) * a.ldy + c;
+      if constexpr (WHOLE) {
         if constexpr (VE == 8)
           *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[VE / 4 - 1]);
         else
@@ -212,10 +327,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdA
           if (i < n) o[i] = static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)));
       }
     } else {
-      Vec<T> o;
-#pragma unroll
-      for (int i = 0; i < VE; ++i) o.e[i] = from_f<T>(fmaf(v[k][i] * rstd, g[i], b[i]));
-      o.template store<AL>(static_cast<T*>(a.y) + row * a.ldy + c, n);
+      store_vec<WHOLE>(static_cast<T*>(a.y) + int64_t(row) * a.ldy + c, v[k], n);
     }
   }
 }
@@ -229,144 +341,339 @@ struct BwdArgs {
   const float* mean;
   const float* rstd;
   float* part;  // [gridDim.x][2][C]
-  int64_t lddy, ldx, lddh, lddx, M;
-  int C, tpr, wf32;
+  int64_t lddy, ldx, lddh, lddx;
+  int M, C, lg, wf32, stages;
+  uint32_t* err;
 };
 
-// Rows as in ln_fwd_kernel, a block taking rows blockIdx.x, blockIdx.x + gridDim.x, ...
-// (in groups of blockDim.x / tpr); the columns' sums stay in registers over
-// all its rows and go to the block's own rows of `part` at the end, so the
-// order of every sum is fixed.
-template <class T, int NV, bool AL>
+// A row's elements of one thread on their way through the backward pass.
+//   g = dy gamma and z = (x - mu) rstd; the sums of g and g z over the row,
+//   dy z and dy added to the columns' sums; then
+//   dx = rstd (g - mean(g) - z mean(g z)) (+ dh)
+template <class T, int NV>
+struct BwdRow {
+  static constexpr int VP = Vec<T>::VP;
+  f2 g[NV][VP], z[NV][VP];
+  f2 s1, s2;
+  __device__ __forceinline__ void clear() { s1 = s2 = 0ull; }
+  template <bool WHOLE>
+  __device__ __forceinline__ void take(int k, const Vec<T>& x, const Vec<T>& dy, const f2 (&ga)[VP], float mu,
+                                       float rstd, f2 (&dg)[VP], f2 (&db)[VP], int n) {
+    const f2 r2 = f2_of(rstd, rstd), nm = f2_of(-mu, -mu);
+    f2 d[VP];
+    x.get(z[k]);
+    dy.get(d);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) z[k][i] = f2_mul(f2_add(z[k][i], nm), r2);
+    clear_past<WHOLE>(z[k], n);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      g[k][i] = f2_mul(d[i], ga[i]);
+      s1 = f2_add(s1, g[k][i]);
+      s2 = f2_fma(g[k][i], z[k][i], s2);
+      dg[i] = f2_fma(d[i], z[k][i], dg[i]);
+      db[i] = f2_add(db[i], d[i]);
+    }
+  }
+  // vector 0 of a row that is not held: g and z once more
+  __device__ __forceinline__ void again(const Vec<T>& x, const Vec<T>& dy, const f2 (&ga)[VP], float mu, float rstd) {
+    const f2 r2 = f2_of(rstd, rstd), nm = f2_of(-mu, -mu);
+    x.get(z[0]);
+    dy.get(g[0]);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      z[0][i] = f2_mul(f2_add(z[0][i], nm), r2);
+      g[0][i] = f2_mul(g[0][i], ga[i]);
+    }
+  }
+  // the row's means m1, m2 (of g and g z) -> dx of vector k
+  __device__ __forceinline__ void give(int k, float m1, float m2, float rstd, const f2 (&dh)[VP],
+                                       f2 (&dx)[VP]) const {
+    const f2 r2 = f2_of(rstd, rstd), a = f2_of(-m1, -m1), b = f2_of(-m2, -m2);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) dx[i] = f2_fma(f2_fma(z[k][i], b, f2_add(g[k][i], a)), r2, dh[i]);
+  }
+};
+
+// The block's partial sums of the columns.
+template <class T, int NV>
+__device__ __forceinline__ void store_part(float* p, int C, int t, int threads, const f2 (&dg)[NV][Vec<T>::VP],
+                                           const f2 (&db)[NV][Vec<T>::VP]) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (t + k * threads) * Vec<T>::VE;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::VP; ++i) {
+      const float2 g = f2_get(dg[k][i]), b = f2_get(db[k][i]);
+      if (c + 2 * i < C) {
+        p[c + 2 * i] = g.x;
+        p[C + c + 2 * i] = b.x;
+      }
+      if (c + 2 * i + 1 < C) {
+        p[c + 2 * i + 1] = g.y;
+        p[C + c + 2 * i + 1] = b.y;
+      }
+    }
+  }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... (LANES: groups of rows, one to
+// 2^lg lanes); the columns' sums stay in registers over all of them and go to
+// the block's own rows of `part` at the end, so the order of every sum is
+// fixed.  The next row's loads are issued before this row's sums.
+template <class T, int NV, bool WHOLE, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdArgs a) {
-  constexpr int VE = Vec<T>::VE;
-  __shared__ float2 red[64];
-  const int threads = a.tpr ? a.tpr : blockDim.x;
-  const int group = threadIdx.x / threads, groups = blockDim.x / threads;
-  const int t = threadIdx.x % threads;
+  constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
+  __shared__ __align__(16) float red[LANES ? 4 : 128];
+  const int threads = LANES ? 1 << a.lg : blockDim.x;
+  const int group = LANES ? threadIdx.x >> a.lg : 0, groups = LANES ? blockDim.x >> a.lg : 1;
+  const int t = LANES ? threadIdx.x & (threads - 1) : threadIdx.x;
+  if constexpr (!LANES) {
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) red[i] = 0.f;
+    __syncthreads();
+  }
   griddep_launch_dependents();
   griddep_wait();
-  RowSum sum{red, a.tpr, 0};
-  // up to 16 columns a thread gamma stays in registers; beyond that it would
-  // push the sums out of them, and is read again (from L1) with every row
-  constexpr bool kKeep = NV * VE <= 16;
-  float g[kKeep ? NV : 1][VE], dg[NV][VE], db[NV][VE];
+  f2 ga[NV][VP], dg[NV][VP], db[NV][VP];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (t + k * threads) * VE;
-    if constexpr (kKeep) load_weight<T>(g[k], a.gamma, a.wf32, c, a.C - c);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) dg[k][i] = db[k][i] = 0.f;
+    for (int i = 0; i < VP; ++i) ga[k][i] = dg[k][i] = db[k][i] = 0ull;
+    if (c < a.C) load_weight<WHOLE, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
   }
   const float inv = 1.f / static_cast<float>(a.C);
-  for (int64_t base = int64_t(blockIdx.x) * groups; base < a.M; base += int64_t(gridDim.x) * groups) {
-    const bool live = base + group < a.M;
-    const int64_t row = live ? base + group : a.M - 1;
-    Vec<T> x[NV], dy[NV];
-    const float mu = a.mean[row], rstd = a.rstd[row];
-    float2 s = make_float2(0.f, 0.f);
+  const int64_t step = int64_t(gridDim.x) * groups;
+  Vec<T> x[NV], dy[NV];
+  float mun = 0.f, rstdn = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (row >= a.M) return;
+    mun = a.mean[row];
+    rstdn = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      const int n = a.C - c;
-      if (n > 0 && live) {
-        x[k].template load<AL>(static_cast<const T*>(a.x) + row * a.ldx + c, n);
-        dy[k].template load<AL>(static_cast<const T*>(a.dy) + row * a.lddy + c, n);
+      if (c >= a.C) continue;
+      x[k] = load_vec<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx + c, a.C - c);
+      dy[k] = load_vec<WHOLE>(static_cast<const T*>(a.dy) + row * a.lddy + c, a.C - c);
+    }
+  };
+  const int64_t first = int64_t(blockIdx.x) * groups;
+  fetch(first + group);
+  int turn = 0;
+  for (int64_t base = first; base < a.M; base += step) {
+    const int64_t row = base + group;
+    const bool live = row < a.M;
+    const float mu = mun, rstd = rstdn;
+    BwdRow<T, NV> r;
+    r.clear();
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int n = a.C - (t + k * threads) * VE;
+        if (n > 0) r.template take<WHOLE>(k, x[k], dy[k], ga[k], mu, rstd, dg[k], db[k], n);
       }
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int kg = kKeep ? k : 0;
-      const int c = (t + k * threads) * VE;
-      const int n = a.C - c;
-      if constexpr (!kKeep) load_weight<T>(g[kg], a.gamma, a.wf32, c, n);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float d = to_f(dy[k].e[i]);
-        const float z = live && i < n ? (to_f(x[k].e[i]) - mu) * rstd : 0.f;
-        s.x = fmaf(d, g[kg][i], s.x);
-        s.y = fmaf(d * g[kg][i], z, s.y);
-        dg[k][i] = fmaf(d, z, dg[k][i]);
-        db[k][i] += d;
-      }
+    fetch(row + step);
+    float s1 = f2_get(r.s1).x + f2_get(r.s1).y, s2 = f2_get(r.s2).x + f2_get(r.s2).y;
+    if constexpr (LANES) {
+      s1 = lanes_sum(s1, a.lg);
+      s2 = lanes_sum(s2, a.lg);
+    } else {
+      s1 = block_sum(s1, red + 64 * turn);
+      s2 = block_sum(s2, red + 64 * turn + 32);
+      turn ^= 1;
     }
-    s = sum(s);
-    const float m1 = s.x * inv, m2 = s.y * inv;
     if (!live) continue;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
       const int n = a.C - c;
-      const int kg = kKeep ? k : 0;
       if (n <= 0) continue;
-      if constexpr (!kKeep) load_weight<T>(g[kg], a.gamma, a.wf32, c, n);
-      Vec<T> o, h;
-      if (a.dh) h.template load<AL>(static_cast<const T*>(a.dh) + row * a.lddh + c, n);
+      f2 h[VP];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float z = (to_f(x[k].e[i]) - mu) * rstd;
-        float d = rstd * (fmaf(to_f(dy[k].e[i]), g[kg][i], -m1) - z * m2);
-        if (a.dh) d += to_f(h.e[i]);
-        o.e[i] = from_f<T>(d);
-      }
-      o.template store<AL>(static_cast<T*>(a.dx) + row * a.lddx + c, n);
+      for (int i = 0; i < VP; ++i) h[i] = 0ull;
+      if (a.dh) load_vec<WHOLE>(static_cast<const T*>(a.dh) + row * a.lddh + c, n).get(h);
+      r.give(k, s1 * inv, s2 * inv, rstd, h, h);
+      store_vec<WHOLE>(static_cast<T*>(a.dx) + row * a.lddx + c, h, n);
     }
   }
-  // groups of lanes that share their columns: summed in the order of the groups
-  if (a.tpr) {
-    extern __shared__ float cols[];  // [groups][2][threads * VE], NV = 1
-    float* mine = cols + size_t(group) * 2 * threads * VE;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      mine[t * VE + i] = dg[0][i];
-      mine[(threads + t) * VE + i] = db[0][i];
-    }
+  if constexpr (LANES) {
+    // groups of lanes that share their columns: summed in the order of the groups
+    extern __shared__ float cols[];  // [groups][2][threads * VE]
+    const int W = threads * VE;
+    store_part<T, NV>(cols + size_t(group) * 2 * W, W, t, threads, dg, db);
     __syncthreads();
-    for (int j = threadIdx.x; j < 2 * threads * VE; j += blockDim.x) {
+    for (int j = threadIdx.x; j < 2 * W; j += blockDim.x) {
       float s = 0.f;
-      for (int w = 0; w < groups; ++w) s += cols[size_t(w) * 2 * threads * VE + j];
-      const int which = j / (threads * VE), c = j % (threads * VE);
+      for (int w = 0; w < groups; ++w) s += cols[size_t(w) * 2 * W + j];
+      const int which = j >= W, c = j - which * W;
       if (c < a.C) a.part[(int64_t(blockIdx.x) * 2 + which) * a.C + c] = s;
     }
-    return;
+  } else {
+    store_part<T, NV>(a.part + int64_t(blockIdx.x) * 2 * a.C, a.C, t, threads, dg, db);
   }
-  float* p = a.part + int64_t(blockIdx.x) * 2 * a.C;
+}
+
+// The same for whole vectors, a block a row: x, dy and dh of the next rows come
+// by bulk copies into a ring of `stages` rows (an SM has to have some 50 KB of
+// reads under way to draw the memory's full rate, more than a block holds in
+// registers).  Up to two vectors a thread a row stays in registers, so its
+// stage is free at the barrier of its own sums; with four, which would not
+// fit, it is read from the ring twice, and gamma with it, and the stage is free
+// at the next row's barrier.
+template <class T, int NV>
+__global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
+  constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) float2 red[2][16];
+  __shared__ uint64_t full[16];
+  const int threads = blockDim.x, t = threadIdx.x;
+  const int warps = threads >> 5;
+  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T);
+  const uint32_t stage_bytes = row_bytes * (a.dh ? 3 : 2);
+  if (t == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  auto fetch = [&](int64_t row, int s) {  // one thread
+    uint8_t* to = ring + s * stage_bytes;
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    bulk_load(smem_addr(to), static_cast<const T*>(a.x) + row * a.ldx, row_bytes, &full[s]);
+    bulk_load(smem_addr(to + row_bytes), static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, &full[s]);
+    if (a.dh) bulk_load(smem_addr(to + 2 * row_bytes), static_cast<const T*>(a.dh) + row * a.lddh, row_bytes, &full[s]);
+  };
+  const int64_t step = gridDim.x;
+  if (t == 0)
+    for (int s = 0; s < a.stages; ++s)
+      if (blockIdx.x + s * step < a.M) fetch(blockIdx.x + s * step, s);
+  constexpr bool kHold = NV <= 2;
+  constexpr int NH = kHold ? NV : 1;
+  f2 ga[NH][VP], dg[NV][VP], db[NV][VP];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (t + k * threads) * VE;
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-      if (c + i < a.C) {
-        p[c + i] = dg[k][i];
-        p[a.C + c + i] = db[k][i];
-      }
+    for (int i = 0; i < VP; ++i) {
+      dg[k][i] = db[k][i] = 0ull;
+      if constexpr (kHold) ga[k][i] = 0ull;
+    }
+    if constexpr (kHold) {
+      if (c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+    }
   }
+  const float inv = 1.f / static_cast<float>(a.C);
+  int s = 0, turn = 0;
+  uint32_t phase = 0;
+  float mu = 0.f, rstd = 0.f;
+  if (blockIdx.x < a.M) {
+    mu = a.mean[blockIdx.x];
+    rstd = a.rstd[blockIdx.x];
+  }
+  int never = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += step) {
+    mbar_wait(&full[s], phase, &never, a.err, ERR_WAIT_FULL);
+    const uint8_t* from = ring + s * stage_bytes;
+    BwdRow<T, NH> r;
+    r.clear();
+    Vec<T> dh[NH];
+    auto read = [&](int c, Vec<T>& x, Vec<T>& dy) {
+      x.raw = *reinterpret_cast<const uint4*>(from + c * sizeof(T));
+      dy.raw = *reinterpret_cast<const uint4*>(from + row_bytes + c * sizeof(T));
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * threads) * VE;
+      if (c >= a.C) continue;
+      const int kh = kHold ? k : 0;
+      Vec<T> x, dy;
+      read(c, x, dy);
+      if constexpr (kHold) {
+        if (a.dh) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+      } else {
+        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
+      }
+      r.template take<true>(kh, x, dy, ga[kh], mu, rstd, dg[k], db[k], VE);
+    }
+    const float mc = mu, rs = rstd;
+    if (row + step < a.M) {
+      mu = a.mean[row + step];
+      rstd = a.rstd[row + step];
+    }
+    float2 v = make_float2(f2_get(r.s1).x + f2_get(r.s1).y, f2_get(r.s2).x + f2_get(r.s2).y);
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if ((t & 31) == 0) red[turn][t >> 5] = v;
+    __syncthreads();
+    if (t == 0) {  // the stage that every thread is done with: this row's, or the one before it
+      const int64_t next = row + (kHold ? a.stages : a.stages - 1) * step;
+      if (next < a.M && (kHold || row != blockIdx.x)) fetch(next, kHold ? s : s ? s - 1 : a.stages - 1);
+    }
+    v = make_float2(0.f, 0.f);
+    for (int w = 0; w < warps; ++w) {
+      v.x += red[turn][w].x;
+      v.y += red[turn][w].y;
+    }
+    turn ^= 1;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (t + k * threads) * VE;
+      if (c >= a.C) continue;
+      f2 h[VP];
+      if constexpr (kHold) {
+        dh[k].get(h);
+        r.give(k, v.x * inv, v.y * inv, rs, h, h);
+      } else {
+        Vec<T> x, dy;
+        read(c, x, dy);
+        if (a.dh) dh[0].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+        dh[0].get(h);
+        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
+        r.again(x, dy, ga[0], mc, rs);
+        r.give(0, v.x * inv, v.y * inv, rs, h, h);
+      }
+      store_vec<true>(dx + c, h, VE);
+    }
+    if (++s == a.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  store_part<T, NV>(a.part + int64_t(blockIdx.x) * 2 * a.C, a.C, t, threads, dg, db);
 }
 
 // dgamma and dbeta from the blocks' partial sums: 32 columns a block, the
 // partial rows dealt to its warps, each sum in a fixed order.
-__global__ void __launch_bounds__(512) ln_colsum_kernel(const float* part, int rows, int C, void* dgamma, void* dbeta,
-                                                        int kind) {
-  __shared__ float sm[16][33];
+__global__ void __launch_bounds__(1024) ln_colsum_kernel(const float* part, int rows, int C, void* dgamma, void* dbeta,
+                                                         int kind) {
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;  // column of the 2 C of a partial row
   griddep_launch_dependents();
   griddep_wait();
-  float s = 0.f;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < 2 * C)
-    for (int r = warp; r < rows; r += 16) s += part[int64_t(r) * 2 * C + c];
-  sm[warp][lane] = s;
+    for (int r0 = warp; r0 < rows; r0 += 128) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r0 + 32 * k < rows) s[k] += part[int64_t(r0 + 32 * k) * 2 * C + c];
+    }
+  sm[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
   if (warp == 0 && c < 2 * C) {
-    s = 0.f;
+    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += sm[w][lane];
+    for (int w = 0; w < 32; ++w) v += sm[w][lane];
     void* out = c < C ? dgamma : dbeta;
     const int i = c < C ? c : c - C;
     if (out) {
-      if (kind == SPG_F32) static_cast<float*>(out)[i] = s;
-      else if (kind == SPG_F16) static_cast<__half*>(out)[i] = from_f<__half>(s);
-      else static_cast<__nv_bfloat16*>(out)[i] = from_f<__nv_bfloat16>(s);
+      if (kind == SPG_F32) static_cast<float*>(out)[i] = v;
+      else if (kind == SPG_F16) static_cast<__half*>(out)[i] = from_f<__half>(v);
+      else static_cast<__nv_bfloat16*>(out)[i] = from_f<__nv_bfloat16>(v);
     }
   }
 }
@@ -375,65 +682,87 @@ constexpr int kMaxC = 16384;
 
 int esize(int dtype) { return dtype == SPG_F32 ? 4 : 2; }
 
-// How a row is dealt to threads: lanes of one warp where NV vectors each are
-// enough for it, else a block.
+// How a row is dealt to threads.
 struct Shape {
-  int tpr;      // lanes of a warp, or 0: the block
+  bool lanes;   // to 2^lg lanes of a warp, otherwise to the block
+  int lg;
   int nv;       // vectors a thread
   int threads;  // of the block
 };
 
 int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
 
+int lg_of(int nvec) {
+  int lg = 0;
+  while ((1 << lg) < nvec && lg < 5) ++lg;
+  return lg;
+}
+
+// Up to four vectors a lane a row stays in one warp (no barrier); beyond that
+// a block with four vectors a thread, so that a row's two block sums weigh little.
 Shape fwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
-  if (nvec <= 32) {
-    int tpr = 1;
-    while (tpr < nvec) tpr *= 2;
-    return {tpr, 1, 128};
-  }
-  if (nvec <= 128) return {32, (nvec + 31) / 32, 128};
-  const int nv = nvec <= 512 ? 2 : 4;
-  return {0, nv, round32((nvec + nv - 1) / nv)};
+  if (nvec <= 128) return {true, lg_of(nvec), (nvec + 31) / 32, 128};
+  return {false, 0, 4, round32((nvec + 3) / 4)};
 }
 
+// One vector a lane where a warp holds the row (several rows a warp where it
+// is shorter), otherwise one or two vectors a thread of a block.
 Shape bwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
-  if (nvec <= 32) {
-    int tpr = 1;
-    while (tpr < nvec) tpr *= 2;
-    return {tpr, 1, 128};
-  }
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  return {0, nv, round32((nvec + nv - 1) / nv)};
+  if (nvec <= 32) return {true, lg_of(nvec), 1, 256};
+  const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  return {false, 0, nv, round32((nvec + nv - 1) / nv)};
 }
 
-// Blocks of the backward kernel: enough to fill the device, a row group each
-// at least.
+// Blocks of the backward kernel: two an SM (more where they are small), a row
+// group each at least.  Each leaves one row of partial sums.
 int bwd_blocks(int64_t M, const Shape& s) {
-  const int64_t groups = s.tpr ? s.threads / s.tpr : 1;
+  const int64_t groups = s.lanes ? s.threads >> s.lg : 1;
   const int64_t work = (M + groups - 1) / groups;
   const int64_t per_sm = 1024 / s.threads;
-  const int64_t cap = int64_t(sm_count()) * (per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm);
+  const int64_t cap = int64_t(sm_count()) * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm);
   return static_cast<int>(work < cap ? work : cap);
 }
 
-template <class T, bool AL>
+template <class T, bool WHOLE>
 cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int64_t blocks, cudaStream_t st) {
-  void (*k)(const FwdArgs) = s.nv == 1   ? ln_fwd_kernel<T, 1, AL>
-                             : s.nv == 2 ? ln_fwd_kernel<T, 2, AL>
-                             : s.nv == 3 ? ln_fwd_kernel<T, 3, AL>
-                                         : ln_fwd_kernel<T, 4, AL>;
+  void (*k)(const FwdArgs) = !s.lanes    ? ln_fwd_kernel<T, 4, WHOLE, false>
+                             : s.nv == 1 ? ln_fwd_kernel<T, 1, WHOLE, true>
+                             : s.nv == 2 ? ln_fwd_kernel<T, 2, WHOLE, true>
+                             : s.nv == 3 ? ln_fwd_kernel<T, 3, WHOLE, true>
+                                         : ln_fwd_kernel<T, 4, WHOLE, true>;
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), 0, st, a);
 }
 
-template <class T, bool AL>
+template <class T, bool WHOLE>
 cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int blocks, cudaStream_t st) {
-  void (*k)(const BwdArgs) = s.nv == 1   ? ln_bwd_kernel<T, 1, AL>
-                             : s.nv == 2 ? ln_bwd_kernel<T, 2, AL>
-                                         : ln_bwd_kernel<T, 4, AL>;
-  const size_t smem = s.tpr ? size_t(s.threads) * 2 * Vec<T>::VE * sizeof(float) : 0;
-  return launch_pdl(k, dim3(blocks), dim3(s.threads), smem, st, a);
+  if (s.lanes)
+    return launch_pdl(ln_bwd_kernel<T, 1, WHOLE, true>, dim3(blocks), dim3(s.threads),
+                      size_t(s.threads) * 2 * Vec<T>::VE * sizeof(float), st, a);
+  void (*k)(const BwdArgs) = s.nv == 1   ? ln_bwd_kernel<T, 1, WHOLE, false>
+                             : s.nv == 2 ? ln_bwd_kernel<T, 2, WHOLE, false>
+                                         : ln_bwd_kernel<T, 4, WHOLE, false>;
+  if constexpr (WHOLE) {
+    // the ring, where at least two rows of it fit: two blocks an SM share the memory
+    const int64_t stage = int64_t(a.C) * sizeof(T) * (a.dh ? 3 : 2);
+    const int64_t budget = 224 * 1024 / (s.threads <= 256 ? 4 : 2) - 1024;
+    int64_t stages = budget / stage;
+    stages = stages > 16 ? 16 : stages;
+    if (stages < 2) stages = (224 * 1024 - 1024) / stage > 16 ? 16 : (224 * 1024 - 1024) / stage;
+    if (s.threads <= 512 && stages >= 2) {
+      k = s.nv == 1   ? ln_bwd_ring_kernel<T, 1>
+          : s.nv == 2 ? ln_bwd_ring_kernel<T, 2>
+                      : ln_bwd_ring_kernel<T, 4>;
+      const int smem = static_cast<int>(stages * stage);
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      BwdArgs b = a;
+      b.stages = static_cast<int>(stages);
+      return launch_pdl(k, dim3(blocks), dim3(s.threads), smem, st, b);
+    }
+  }
+  return launch_pdl(k, dim3(blocks), dim3(s.threads), 0, st, a);
 }
 
 bool vec_ok(const void* p, int64_t ld, int es) { return p == nullptr || (aligned(p, 16) && (ld * es) % 16 == 0); }
@@ -457,16 +786,14 @@ spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void*
   if (M == 0) return SPG_OK;
   spg_status rc = check_device();
   if (rc != SPG_OK) return rc;
-  const FwdArgs a{X,   res, H,   Y, gamma,         beta,          mean, rstd, ldx, ldres, ldh,
-                  ldy, M, int(C), 0, wdtype == SPG_F32, s8, eps, qscale};
-  Shape s = fwd_shape(int(C), es);
-  FwdArgs b = a;
-  b.tpr = s.tpr;
-  const int64_t rows = s.tpr ? s.threads / s.tpr : 1;
+  const Shape s = fwd_shape(int(C), es);
+  const FwdArgs b{X,   res, H,      Y,      gamma, beta,              mean, rstd, ldx,   ldres,
+                  ldh, ldy, int(M), int(C), s.lg,  wdtype == SPG_F32, s8,   eps,  qscale};
+  const int64_t rows = s.lanes ? s.threads >> s.lg : 1;
   const int64_t blocks = (M + rows - 1) / rows;
-  // rows that start on 16-byte boundaries move in 16-byte vectors, others element by element
-  const bool al = vec_ok(X, ldx, es) && vec_ok(res, ldres, es) && vec_ok(H, ldh, es) &&
-                  (s8 ? aligned(Y, 8) && ldy % 8 == 0 : vec_ok(Y, ldy, es));
+  // whole 16-byte vectors in rows that start on 16-byte boundaries; otherwise element by element
+  const bool al = (C * es) % 16 == 0 && vec_ok(X, ldx, es) && vec_ok(res, ldres, es) && vec_ok(H, ldh, es) &&
+                  (s8 ? aligned(Y, 8) && ldy % 8 == 0 : vec_ok(Y, ldy, es)) && aligned(gamma, 16) && aligned(beta, 16);
   cudaError_t e;
   if (dtype == SPG_F32) e = al ? launch_fwd<float, true>(b, s, blocks, st) : launch_fwd<float, false>(b, s, blocks, st);
   else if (dtype == SPG_F16)
@@ -526,9 +853,12 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
   int blocks = 0;
   if (M != 0) {
     blocks = bwd_blocks(M, s);
-    const BwdArgs a{dY,  X,    dH,  dX,   gamma, mean,   rstd,  static_cast<float*>(workspace), lddy,
-                    ldx, lddh, lddx, M, int(C), s.tpr, wdtype == SPG_F32};
-    const bool al = vec_ok(dY, lddy, es) && vec_ok(X, ldx, es) && vec_ok(dH, lddh, es) && vec_ok(dX, lddx, es);
+    uint32_t* err = device_error_word();
+    if (!err) return SPG_ERR_CUDA;
+    const BwdArgs a{dY,  X,    dH,   dX,     gamma,  mean, rstd, static_cast<float*>(workspace), lddy,
+                    ldx, lddh, lddx, int(M), int(C), s.lg, wdtype == SPG_F32, 0, err};
+    const bool al = (C * es) % 16 == 0 && vec_ok(dY, lddy, es) && vec_ok(X, ldx, es) && vec_ok(dH, lddh, es) && vec_ok(dX, lddx, es) &&
+                    aligned(gamma, 16);
     cudaError_t e;
     if (dtype == SPG_F32) e = al ? launch_bwd<float, true>(a, s, blocks, st) : launch_bwd<float, false>(a, s, blocks, st);
     else if (dtype == SPG_F16)
@@ -538,7 +868,7 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
     if (e != cudaSuccess) return SPG_ERR_CUDA;
   }
   // no rows: the sums over them are zero
-  if (launch_pdl(ln_colsum_kernel, dim3(static_cast<unsigned>((2 * C + 31) / 32)), dim3(512), 0, st,
+  if (launch_pdl(ln_colsum_kernel, dim3(static_cast<unsigned>((2 * C + 31) / 32)), dim3(1024), 0, st,
                  static_cast<const float*>(workspace), blocks, int(C), dgamma, dbeta, int(wdtype)) != cudaSuccess)
     return SPG_ERR_CUDA;
   return launch_status();
