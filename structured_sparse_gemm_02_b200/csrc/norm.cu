@@ -112,11 +112,15 @@ struct Vec {
 
 // VE elements at p, of which the first n are inside the row.  WHOLE: all of
 // them are, and p is 16-byte aligned; otherwise they move one by one and the
-// others are 0.
-template <bool WHOLE, class T>
+// others are 0.  ONCE: data that is read once, which leaves L1 to the weights.
+template <bool WHOLE, bool ONCE, class T>
 __device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
   Vec<T> v;
-  if constexpr (WHOLE) {
+  if constexpr (WHOLE && ONCE) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.raw.x), "=r"(v.raw.y), "=r"(v.raw.z), "=r"(v.raw.w)
+                 : "l"(p));
+  } else if constexpr (WHOLE) {
     v.raw = *reinterpret_cast<const uint4*>(p);
   } else {
     f2 f[Vec<T>::VP];
@@ -143,23 +147,24 @@ __device__ __forceinline__ void store_vec(T* p, const f2 (&f)[Vec<T>::VP], int n
   }
 }
 
-// VE elements of gamma or beta, in the activations' type or in fp32; 0 where the pointer is null.
-template <bool WHOLE, class T>
-__device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int f32, int c, int n) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int i = 0; i < Vec<T>::VP; ++i) w[i] = 0ull;
-  } else if (f32 || sizeof(T) == 4) {
+// VE elements of gamma or beta, in fp32 (W32) or in the activations' type.
+template <bool WHOLE, bool W32, class T>
+__device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int c, int n) {
+  if constexpr (W32 || sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < Vec<T>::VP; k += 2) {
       f2 q[2];
-      load_vec<WHOLE>(static_cast<const float*>(p) + c + 2 * k, n - 2 * k).get(q);
+      load_vec<WHOLE, false>(static_cast<const float*>(p) + c + 2 * k, n - 2 * k).get(q);
       w[k] = q[0];
       w[k + 1] = q[1];
     }
   } else {
-    load_vec<WHOLE>(static_cast<const T*>(p) + c, n).get(w);
+    load_vec<WHOLE, false>(static_cast<const T*>(p) + c, n).get(w);
   }
+}
+template <bool WHOLE, class T>
+__device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int f32, int c, int n) {
+  f32 ? load_weight<WHOLE, true, T>(w, p, c, n) : load_weight<WHOLE, false, T>(w, p, c, n);
 }
 
 // 0 for the elements of a vector past its row's end.
@@ -189,6 +194,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// red[0] + ... + red[n - 1], read in 16-byte pieces (0 up to the next multiple of four).
+__device__ __forceinline__ float sum_of(const float* red, int n) {
+  float4 s = *reinterpret_cast<const float4*>(red);
+  for (int w = 4; w < n; w += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(red + w);
+    s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+  }
+  return (s.x + s.y) + (s.z + s.w);
+}
 // Sum over the block through `red` (one float a warp, up to a multiple of
 // four, the unused ones 0); the caller alternates between two such arrays, so
 // one barrier a sum is enough.
@@ -196,12 +210,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float4 s = *reinterpret_cast<const float4*>(red);
-  for (int w = 4; w < int(blockDim.x >> 5); w += 4) {
-    const float4 q = *reinterpret_cast<const float4*>(red + w);
-    s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
-  }
-  return (s.x + s.y) + (s.z + s.w);
+  return sum_of(red, blockDim.x >> 5);
 }
 
 struct FwdArgs {
@@ -218,12 +227,62 @@ struct FwdArgs {
   float eps, qscale;
 };
 
+// How rows meet vectors: element by element; in whole vectors (C is a multiple
+// of the vector and every row 16-byte aligned); or so that besides every
+// thread has all of its NV vectors, which saves the checks.
+enum Mode { ELEMENTS = 0, WHOLE_VECTORS = 1, FULL_ROWS = 2 };
+
+// y = (h - mu) rstd gamma + beta of a thread's vectors (v holds h - mu), stored in its type or as int8 codes.
+template <class T, int NV, int MODE, bool W32, bool BETA, bool S8>
+__device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::VP], int64_t row, int t, int threads,
+                                          f2 r2) {
+  constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
+  constexpr bool WHOLE = MODE != ELEMENTS, FULL = MODE == FULL_ROWS;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (t + k * threads) * VE;
+    const int n = a.C - c;
+    if (!FULL && n <= 0) continue;
+    f2 g[VP], b[VP];
+    load_weight<WHOLE, W32, T>(g, a.gamma, c, n);
+    if constexpr (BETA) load_weight<WHOLE, W32, T>(b, a.beta, c, n);
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const f2 z = f2_mul(v[k][i], r2);
+      v[k][i] = BETA ? f2_fma(z, g[i], b[i]) : f2_mul(z, g[i]);
+    }
+    if constexpr (S8) {
+      // clamp(rne(y qscale)); a NaN gives code 0
+      uint32_t w[VE / 4];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const float2 e = f2_get(v[k][i / 2]);
+        const int code = max(-127, min(127, __float2int_rn((i & 1 ? e.y : e.x) * a.qscale)));
+        w[i / 4] = (i % 4 ? w[i / 4] : 0u) | (static_cast<uint32_t>(code & 0xFF) << (8 * (i % 4)));
+      }
+      int8_t* o = static_cast<int8_t*>(a.y) + row * a.ldy + c;
+      if constexpr (WHOLE) {
+        if constexpr (VE == 8)
+          *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[VE / 4 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(o) = w[0];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (i < n) o[i] = static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)));
+      }
+    } else {
+      store_vec<WHOLE>(static_cast<T*>(a.y) + row * a.ldy + c, v[k], n);
+    }
+  }
+}
+
 // LANES: a row belongs to 2^lg lanes of a warp, otherwise to the block;
 // thread t of the row holds vectors t, t + threads, ... (NV of them).
-// WHOLE: C is a multiple of the vector and every row 16-byte aligned.
-template <class T, int NV, bool WHOLE, bool LANES>
-__global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdArgs a) {
+template <class T, int NV, int MODE, bool LANES>
+__global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 ? 1 : 2) ln_fwd_kernel(const FwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
+  constexpr bool WHOLE = MODE != ELEMENTS, FULL = MODE == FULL_ROWS;
   __shared__ __align__(16) float red[LANES ? 4 : 64];
   const int threads = LANES ? 1 << a.lg : blockDim.x;
   const int t = LANES ? threadIdx.x & (threads - 1) : threadIdx.x;
@@ -245,7 +304,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdA
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
       Vec<T> e;
-      if (c < a.C) e = load_vec<WHOLE>(x + c, a.C - c);
+      if (FULL || c < a.C) e = load_vec<WHOLE, true>(x + c, a.C - c);
       e.get(v[k]);
     }
   }
@@ -256,9 +315,9 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdA
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (c >= a.C) continue;
+      if (!FULL && c >= a.C) continue;
       f2 r[VP];
-      load_vec<WHOLE>(res + c, a.C - c).get(r);
+      load_vec<WHOLE, true>(res + c, a.C - c).get(r);
       // the backward pass reads h as it is stored, so the norm is taken of the rounded sum
       Vec<T> e;
 #pragma unroll
@@ -281,7 +340,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdA
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int n = a.C - (t + k * threads) * VE;
-    if (n <= 0) continue;
+    if (!FULL && n <= 0) continue;
 #pragma unroll
     for (int i = 0; i < VP; ++i) v[k][i] = f2_add(v[k][i], nmu);
     clear_past<WHOLE>(v[k], n);
@@ -296,39 +355,18 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_fwd_kernel(const FwdA
     if (a.rstd) a.rstd[row] = rstd;
   }
   const f2 r2 = f2_of(rstd, rstd);
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = (t + k * threads) * VE;
-    const int n = a.C - c;
-    if (n <= 0) continue;
-    f2 g[VP], b[VP];
-    load_weight<WHOLE, T>(g, a.gamma, a.wf32, c, n);
-    load_weight<WHOLE, T>(b, a.beta, a.wf32, c, n);
-#pragma unroll
-    for (int i = 0; i < VP; ++i) v[k][i] = f2_fma(f2_mul(v[k][i], r2), g[i], b[i]);
-    if (a.s8) {
-      // clamp(rne(y qscale)); a NaN gives code 0
-      uint32_t w[VE / 4];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float2 e = f2_get(v[k][i / 2]);
-        const int code = max(-127, min(127, __float2int_rn((i & 1 ? e.y : e.x) * a.qscale)));
-        w[i / 4] = (i % 4 ? w[i / 4] : 0u) | (static_cast<uint32_t>(code & 0xFF) << (8 * (i % 4)));
-      }
-      int8_t* o = static_cast<int8_t*>(a.y) + int64_t(row) * a.ldy + c;
-      if constexpr (WHOLE) {
-        if constexpr (VE == 8)
-          *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[VE / 4 - 1]);
-        else
-          *reinterpret_cast<uint32_t*>(o) = w[0];
-      } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (i < n) o[i] = static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)));
-      }
-    } else {
-      store_vec<WHOLE>(static_cast<T*>(a.y) + int64_t(row) * a.ldy + c, v[k], n);
-    }
+  // one copy of the last step for each kind of weights and output, so that its
+  // loop has no branch (they cost a third of the kernel's instructions)
+  if (a.s8) {
+    if (a.wf32) a.beta ? ln_finish<T, NV, MODE, true, true, true>(a, v, row, t, threads, r2)
+                       : ln_finish<T, NV, MODE, true, false, true>(a, v, row, t, threads, r2);
+    else a.beta ? ln_finish<T, NV, MODE, false, true, true>(a, v, row, t, threads, r2)
+                : ln_finish<T, NV, MODE, false, false, true>(a, v, row, t, threads, r2);
+  } else {
+    if (a.wf32) a.beta ? ln_finish<T, NV, MODE, true, true, false>(a, v, row, t, threads, r2)
+                       : ln_finish<T, NV, MODE, true, false, false>(a, v, row, t, threads, r2);
+    else a.beta ? ln_finish<T, NV, MODE, false, true, false>(a, v, row, t, threads, r2)
+                : ln_finish<T, NV, MODE, false, false, false>(a, v, row, t, threads, r2);
   }
 }
 
@@ -454,8 +492,8 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
       if (c >= a.C) continue;
-      x[k] = load_vec<WHOLE>(static_cast<const T*>(a.x) + row * a.ldx + c, a.C - c);
-      dy[k] = load_vec<WHOLE>(static_cast<const T*>(a.dy) + row * a.lddy + c, a.C - c);
+      x[k] = load_vec<WHOLE, true>(static_cast<const T*>(a.x) + row * a.ldx + c, a.C - c);
+      dy[k] = load_vec<WHOLE, true>(static_cast<const T*>(a.dy) + row * a.lddy + c, a.C - c);
     }
   };
   const int64_t first = int64_t(blockIdx.x) * groups;
@@ -493,7 +531,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
       f2 h[VP];
 #pragma unroll
       for (int i = 0; i < VP; ++i) h[i] = 0ull;
-      if (a.dh) load_vec<WHOLE>(static_cast<const T*>(a.dh) + row * a.lddh + c, n).get(h);
+      if (a.dh) load_vec<WHOLE, true>(static_cast<const T*>(a.dh) + row * a.lddh + c, n).get(h);
       r.give(k, s1 * inv, s2 * inv, rstd, h, h);
       store_vec<WHOLE>(static_cast<T*>(a.dx) + row * a.lddx + c, h, n);
     }
@@ -522,16 +560,16 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
 // stage is free at the barrier of its own sums; with four, which would not
 // fit, it is read from the ring twice, and gamma with it, and the stage is free
 // at the next row's barrier.
-template <class T, int NV>
+template <class T, int NV, bool FULL, bool DH>
 __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) float2 red[2][16];
+  __shared__ __align__(16) float red[2][2][16];  // two turns of the sums of g and of g z, one float a warp
   __shared__ uint64_t full[16];
   const int threads = blockDim.x, t = threadIdx.x;
-  const int warps = threads >> 5;
+  for (int i = t; i < 64; i += threads) red[0][0][i] = 0.f;
   const uint32_t row_bytes = uint32_t(a.C) * sizeof(T);
-  const uint32_t stage_bytes = row_bytes * (a.dh ? 3 : 2);
+  const uint32_t stage_bytes = row_bytes * (DH ? 3 : 2);
   if (t == 0) {
     for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
     fence_barrier_init();
@@ -544,7 +582,7 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
     mbar_arrive_expect_tx(&full[s], stage_bytes);
     bulk_load(smem_addr(to), static_cast<const T*>(a.x) + row * a.ldx, row_bytes, &full[s]);
     bulk_load(smem_addr(to + row_bytes), static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, &full[s]);
-    if (a.dh) bulk_load(smem_addr(to + 2 * row_bytes), static_cast<const T*>(a.dh) + row * a.lddh, row_bytes, &full[s]);
+    if (DH) bulk_load(smem_addr(to + 2 * row_bytes), static_cast<const T*>(a.dh) + row * a.lddh, row_bytes, &full[s]);
   };
   const int64_t step = gridDim.x;
   if (t == 0)
@@ -562,7 +600,7 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
       if constexpr (kHold) ga[k][i] = 0ull;
     }
     if constexpr (kHold) {
-      if (c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+      if (FULL || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
     }
   }
   const float inv = 1.f / static_cast<float>(a.C);
@@ -587,12 +625,12 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (c >= a.C) continue;
+      if (!FULL && c >= a.C) continue;
       const int kh = kHold ? k : 0;
       Vec<T> x, dy;
       read(c, x, dy);
       if constexpr (kHold) {
-        if (a.dh) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+        if (DH) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
       } else {
         load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
       }
@@ -603,38 +641,39 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
       mu = a.mean[row + step];
       rstd = a.rstd[row + step];
     }
-    float2 v = make_float2(f2_get(r.s1).x + f2_get(r.s1).y, f2_get(r.s2).x + f2_get(r.s2).y);
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if ((t & 31) == 0) red[turn][t >> 5] = v;
+    const float w1 = warp_sum(f2_get(r.s1).x + f2_get(r.s1).y), w2 = warp_sum(f2_get(r.s2).x + f2_get(r.s2).y);
+    if ((t & 31) == 0) {
+      red[turn][0][t >> 5] = w1;
+      red[turn][1][t >> 5] = w2;
+    }
     __syncthreads();
     if (t == 0) {  // the stage that every thread is done with: this row's, or the one before it
       const int64_t next = row + (kHold ? a.stages : a.stages - 1) * step;
       if (next < a.M && (kHold || row != blockIdx.x)) fetch(next, kHold ? s : s ? s - 1 : a.stages - 1);
     }
-    v = make_float2(0.f, 0.f);
-    for (int w = 0; w < warps; ++w) {
-      v.x += red[turn][w].x;
-      v.y += red[turn][w].y;
-    }
+    const float m1 = sum_of(red[turn][0], threads >> 5) * inv, m2 = sum_of(red[turn][1], threads >> 5) * inv;
     turn ^= 1;
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (c >= a.C) continue;
+      if (!FULL && c >= a.C) continue;
       f2 h[VP];
+#pragma unroll
+      for (int i = 0; i < VP; ++i) h[i] = 0ull;
       if constexpr (kHold) {
-        dh[k].get(h);
-        r.give(k, v.x * inv, v.y * inv, rs, h, h);
+        if (DH) dh[k].get(h);
+        r.give(k, m1, m2, rs, h, h);
       } else {
         Vec<T> x, dy;
         read(c, x, dy);
-        if (a.dh) dh[0].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
-        dh[0].get(h);
+        if (DH) {
+          dh[0].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+          dh[0].get(h);
+        }
         load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
         r.again(x, dy, ga[0], mc, rs);
-        r.give(0, v.x * inv, v.y * inv, rs, h, h);
+        r.give(0, m1, m2, rs, h, h);
       }
       store_vec<true>(dx + c, h, VE);
     }
@@ -644,6 +683,110 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
     }
   }
   store_part<T, NV>(a.part + int64_t(blockIdx.x) * 2 * a.C, a.C, t, threads, dg, db);
+}
+
+// The same with a warp a row (up to 128 vectors), so no barrier a row: each
+// warp has its own ring, and the warps' column sums are added in their order
+// at the end.  A row of 768 fp16 values took the block kernel 1.5 us a block.
+constexpr int bwd_warps(int es, int nv) { return es == 4 || nv == 2 ? 16 : 8; }  // what the registers allow
+template <class T, int NV, bool FULL, bool DH>
+__global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_kernel(const BwdArgs a) {
+  constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP, kBwdWarps = bwd_warps(sizeof(T), NV);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t bars[kBwdWarps][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T);
+  const uint32_t stage_bytes = row_bytes * (DH ? 3 : 2);
+  uint8_t* ring = smem + size_t(warp) * a.stages * stage_bytes;
+  uint64_t* full = bars[warp];
+  if (lane == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  griddep_launch_dependents();
+  griddep_wait();
+  auto fetch = [&](int64_t row, int s) {  // one lane
+    uint8_t* to = ring + s * stage_bytes;
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    bulk_load(smem_addr(to), static_cast<const T*>(a.x) + row * a.ldx, row_bytes, &full[s]);
+    bulk_load(smem_addr(to + row_bytes), static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, &full[s]);
+    if (DH) bulk_load(smem_addr(to + 2 * row_bytes), static_cast<const T*>(a.dh) + row * a.lddh, row_bytes, &full[s]);
+  };
+  const int64_t step = int64_t(gridDim.x) * kBwdWarps;
+  const int64_t first = int64_t(blockIdx.x) * kBwdWarps + warp;
+  if (lane == 0)
+    for (int s = 0; s < a.stages; ++s)
+      if (first + s * step < a.M) fetch(first + s * step, s);
+  f2 ga[NV][VP], dg[NV][VP], db[NV][VP];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (lane + 32 * k) * VE;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) ga[k][i] = dg[k][i] = db[k][i] = 0ull;
+    if (FULL || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+  }
+  const float inv = 1.f / static_cast<float>(a.C);
+  int s = 0;
+  uint32_t phase = 0;
+  float mu = 0.f, rstd = 0.f;
+  if (first < a.M) {
+    mu = a.mean[first];
+    rstd = a.rstd[first];
+  }
+  int never = 0;
+  for (int64_t row = first; row < a.M; row += step) {
+    mbar_wait(&full[s], phase, &never, a.err, ERR_WAIT_FULL);
+    const uint8_t* from = ring + s * stage_bytes;
+    BwdRow<T, NV> r;
+    r.clear();
+    Vec<T> dh[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (lane + 32 * k) * VE;
+      if (!FULL && c >= a.C) continue;
+      Vec<T> x, dy;
+      x.raw = *reinterpret_cast<const uint4*>(from + c * sizeof(T));
+      dy.raw = *reinterpret_cast<const uint4*>(from + row_bytes + c * sizeof(T));
+      if (DH) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+      r.template take<true>(k, x, dy, ga[k], mu, rstd, dg[k], db[k], VE);
+    }
+    const float rs = rstd;
+    if (row + step < a.M) {
+      mu = a.mean[row + step];
+      rstd = a.rstd[row + step];
+    }
+    // every lane takes part in the sums, so after them the stage has been read
+    const float m1 = warp_sum(f2_get(r.s1).x + f2_get(r.s1).y) * inv;
+    const float m2 = warp_sum(f2_get(r.s2).x + f2_get(r.s2).y) * inv;
+    if (lane == 0 && row + a.stages * step < a.M) fetch(row + a.stages * step, s);
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (lane + 32 * k) * VE;
+      if (!FULL && c >= a.C) continue;
+      f2 h[VP];
+#pragma unroll
+      for (int i = 0; i < VP; ++i) h[i] = 0ull;
+      if (DH) dh[k].get(h);
+      r.give(k, m1, m2, rs, h, h);
+      store_vec<true>(dx + c, h, VE);
+    }
+    if (++s == a.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  __syncthreads();  // every warp is done with its ring
+  float* cols = reinterpret_cast<float*>(smem);  // [warps][2][C]
+  store_part<T, NV>(cols + size_t(warp) * 2 * a.C, a.C, lane, 32, dg, db);
+  __syncthreads();
+  for (int j = threadIdx.x; j < 2 * a.C; j += blockDim.x) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBwdWarps; ++w) v += cols[size_t(w) * 2 * a.C + j];
+    a.part[int64_t(blockIdx.x) * 2 * a.C + j] = v;
+  }
 }
 
 // dgamma and dbeta from the blocks' partial sums: 32 columns a block, the
@@ -706,63 +849,102 @@ Shape fwd_shape(int C, int es) {
   return {false, 0, 4, round32((nvec + 3) / 4)};
 }
 
-// One vector a lane where a warp holds the row (several rows a warp where it
-// is shorter), otherwise one or two vectors a thread of a block.
+// One vector a lane where that holds the row (several rows a warp where it is
+// shorter); a warp with up to four a lane where the rows are whole vectors;
+// otherwise one to four vectors a thread of a block.
 Shape bwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
   if (nvec <= 32) return {true, lg_of(nvec), 1, 256};
+  if (nvec <= 128 && (C * es) % 16 == 0) {
+    const int nv = (nvec + 31) / 32;
+    return {true, 5, nv, 32 * bwd_warps(es, nv)};
+  }
   const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
   return {false, 0, nv, round32((nvec + nv - 1) / nv)};
 }
 
-// Blocks of the backward kernel: two an SM (more where they are small), a row
-// group each at least.  Each leaves one row of partial sums.
+// Blocks of the backward kernel: as many as are resident, so that each leaves
+// one row of partial sums and no more, and a row group each at least.
+int bwd_per_sm(const Shape& s) {
+  return s.lanes ? (s.nv == 1 ? 3 : 1) : s.threads > 256 ? 1 : s.nv > 1 ? 2 : s.threads > 128 ? 4 : 8;
+}
 int bwd_blocks(int64_t M, const Shape& s) {
   const int64_t groups = s.lanes ? s.threads >> s.lg : 1;
   const int64_t work = (M + groups - 1) / groups;
-  const int64_t per_sm = 1024 / s.threads;
-  const int64_t cap = int64_t(sm_count()) * (per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm);
+  const int64_t cap = int64_t(sm_count()) * bwd_per_sm(s);
   return static_cast<int>(work < cap ? work : cap);
 }
 
-template <class T, bool WHOLE>
+template <class T, int MODE>
 cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int64_t blocks, cudaStream_t st) {
-  void (*k)(const FwdArgs) = !s.lanes    ? ln_fwd_kernel<T, 4, WHOLE, false>
-                             : s.nv == 1 ? ln_fwd_kernel<T, 1, WHOLE, true>
-                             : s.nv == 2 ? ln_fwd_kernel<T, 2, WHOLE, true>
-                             : s.nv == 3 ? ln_fwd_kernel<T, 3, WHOLE, true>
-                                         : ln_fwd_kernel<T, 4, WHOLE, true>;
+  void (*k)(const FwdArgs) = !s.lanes    ? ln_fwd_kernel<T, 4, MODE, false>
+                             : s.nv == 1 ? ln_fwd_kernel<T, 1, MODE, true>
+                             : s.nv == 2 ? ln_fwd_kernel<T, 2, MODE, true>
+                             : s.nv == 3 ? ln_fwd_kernel<T, 3, MODE, true>
+                                         : ln_fwd_kernel<T, 4, MODE, true>;
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), 0, st, a);
+}
+
+// Every thread of a row has all of its vectors.
+bool full_rows(const Shape& s, int C, int es) { return (s.lanes ? 1 << s.lg : s.threads) * s.nv * 16 == C * es; }
+
+using BwdKernel = void (*)(const BwdArgs);
+template <class T, int NV>
+BwdKernel ring_kernel(bool full, bool dh) {
+  return full ? (dh ? ln_bwd_ring_kernel<T, NV, true, true> : ln_bwd_ring_kernel<T, NV, true, false>)
+              : (dh ? ln_bwd_ring_kernel<T, NV, false, true> : ln_bwd_ring_kernel<T, NV, false, false>);
+}
+template <class T, int NV>
+BwdKernel warp_kernel(bool full, bool dh) {
+  return full ? (dh ? ln_bwd_warp_kernel<T, NV, true, true> : ln_bwd_warp_kernel<T, NV, true, false>)
+              : (dh ? ln_bwd_warp_kernel<T, NV, false, true> : ln_bwd_warp_kernel<T, NV, false, false>);
 }
 
 template <class T, bool WHOLE>
 cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int blocks, cudaStream_t st) {
-  if (s.lanes)
-    return launch_pdl(ln_bwd_kernel<T, 1, WHOLE, true>, dim3(blocks), dim3(s.threads),
-                      size_t(s.threads) * 2 * Vec<T>::VE * sizeof(float), st, a);
-  void (*k)(const BwdArgs) = s.nv == 1   ? ln_bwd_kernel<T, 1, WHOLE, false>
-                             : s.nv == 2 ? ln_bwd_kernel<T, 2, WHOLE, false>
-                                         : ln_bwd_kernel<T, 4, WHOLE, false>;
-  if constexpr (WHOLE) {
-    // the ring, where at least two rows of it fit: two blocks an SM share the memory
-    const int64_t stage = int64_t(a.C) * sizeof(T) * (a.dh ? 3 : 2);
-    const int64_t budget = 224 * 1024 / (s.threads <= 256 ? 4 : 2) - 1024;
-    int64_t stages = budget / stage;
-    stages = stages > 16 ? 16 : stages;
-    if (stages < 2) stages = (224 * 1024 - 1024) / stage > 16 ? 16 : (224 * 1024 - 1024) / stage;
-    if (s.threads <= 512 && stages >= 2) {
-      k = s.nv == 1   ? ln_bwd_ring_kernel<T, 1>
-          : s.nv == 2 ? ln_bwd_ring_kernel<T, 2>
-                      : ln_bwd_ring_kernel<T, 4>;
-      const int smem = static_cast<int>(stages * stage);
-      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-      BwdArgs b = a;
-      b.stages = static_cast<int>(stages);
-      return launch_pdl(k, dim3(blocks), dim3(s.threads), smem, st, b);
+  const bool full = full_rows(s, a.C, sizeof(T)), dh = a.dh != nullptr;
+  BwdKernel k;
+  size_t smem = 0;
+  BwdArgs b = a;
+  if (s.lanes && s.nv == 1) {
+    k = ln_bwd_kernel<T, 1, WHOLE, true>;
+    smem = size_t(s.threads) * 2 * Vec<T>::VE * sizeof(float);
+  } else if (s.lanes) {
+    if constexpr (WHOLE) {
+      // one block an SM; two stages of the longest rows (2 KB) take 16 * 2 * 6 KB
+      const int64_t stage = int64_t(a.C) * sizeof(T) * (dh ? 3 : 2) * (s.threads / 32);
+      const int64_t stages = 200 * 1024 / stage;
+      b.stages = stages > 8 ? 8 : static_cast<int>(stages);
+      const int64_t sums = int64_t(s.threads / 32) * 2 * a.C * 4;
+      smem = size_t(b.stages * stage > sums ? b.stages * stage : sums);
+      k = s.nv == 2 ? warp_kernel<T, 2>(full, dh) : s.nv == 3 ? warp_kernel<T, 3>(full, dh) : warp_kernel<T, 4>(full, dh);
+    } else {  // rows of whole vectors that are not 16-byte aligned: the block kernel
+      Shape q = s;
+      q.lanes = false;
+      q.nv = 1;
+      q.threads = round32((a.C * int(sizeof(T)) + 15) / 16);
+      return launch_bwd<T, false>(a, q, blocks, st);
+    }
+  } else {
+    k = s.nv == 1   ? ln_bwd_kernel<T, 1, WHOLE, false>
+        : s.nv == 2 ? ln_bwd_kernel<T, 2, WHOLE, false>
+                    : ln_bwd_kernel<T, 4, WHOLE, false>;
+    if constexpr (WHOLE) {
+      // the ring, where at least two rows of it fit the block's share of shared memory
+      const int64_t stage = int64_t(a.C) * sizeof(T) * (dh ? 3 : 2);
+      const int64_t stages = (224 * 1024 / bwd_per_sm(s) - 1024) / stage;
+      if (s.threads <= 512 && stages >= 2) {
+        b.stages = stages > 16 ? 16 : static_cast<int>(stages);
+        smem = size_t(b.stages * stage);
+        k = s.nv == 1 ? ring_kernel<T, 1>(full, dh) : s.nv == 2 ? ring_kernel<T, 2>(full, dh) : ring_kernel<T, 4>(full, dh);
+      }
     }
   }
-  return launch_pdl(k, dim3(blocks), dim3(s.threads), 0, st, a);
+  if (smem > 40 * 1024) {  // 48 KB with the static arrays
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k, dim3(blocks), dim3(s.threads), smem, st, b);
 }
 
 bool vec_ok(const void* p, int64_t ld, int es) { return p == nullptr || (aligned(p, 16) && (ld * es) % 16 == 0); }
@@ -794,12 +976,20 @@ spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void*
   // whole 16-byte vectors in rows that start on 16-byte boundaries; otherwise element by element
   const bool al = (C * es) % 16 == 0 && vec_ok(X, ldx, es) && vec_ok(res, ldres, es) && vec_ok(H, ldh, es) &&
                   (s8 ? aligned(Y, 8) && ldy % 8 == 0 : vec_ok(Y, ldy, es)) && aligned(gamma, 16) && aligned(beta, 16);
+  const int mode = !al ? ELEMENTS : full_rows(s, int(C), es) ? FULL_ROWS : WHOLE_VECTORS;
   cudaError_t e;
-  if (dtype == SPG_F32) e = al ? launch_fwd<float, true>(b, s, blocks, st) : launch_fwd<float, false>(b, s, blocks, st);
+  if (dtype == SPG_F32)
+    e = mode == ELEMENTS        ? launch_fwd<float, ELEMENTS>(b, s, blocks, st)
+        : mode == WHOLE_VECTORS ? launch_fwd<float, WHOLE_VECTORS>(b, s, blocks, st)
+                                : launch_fwd<float, FULL_ROWS>(b, s, blocks, st);
   else if (dtype == SPG_F16)
-    e = al ? launch_fwd<__half, true>(b, s, blocks, st) : launch_fwd<__half, false>(b, s, blocks, st);
+    e = mode == ELEMENTS        ? launch_fwd<__half, ELEMENTS>(b, s, blocks, st)
+        : mode == WHOLE_VECTORS ? launch_fwd<__half, WHOLE_VECTORS>(b, s, blocks, st)
+                                : launch_fwd<__half, FULL_ROWS>(b, s, blocks, st);
   else
-    e = al ? launch_fwd<__nv_bfloat16, true>(b, s, blocks, st) : launch_fwd<__nv_bfloat16, false>(b, s, blocks, st);
+    e = mode == ELEMENTS        ? launch_fwd<__nv_bfloat16, ELEMENTS>(b, s, blocks, st)
+        : mode == WHOLE_VECTORS ? launch_fwd<__nv_bfloat16, WHOLE_VECTORS>(b, s, blocks, st)
+                                : launch_fwd<__nv_bfloat16, FULL_ROWS>(b, s, blocks, st);
   return e == cudaSuccess ? launch_status() : SPG_ERR_CUDA;
 }
 
