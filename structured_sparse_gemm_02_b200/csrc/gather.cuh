@@ -10,9 +10,9 @@
 namespace spg {
 
 // 3-D tiled tensor map over contiguous [d2][d1][d0] 16-bit elements (d0 a
-// multiple of 8); box of box0 x box1 x 1 with the 128-byte swizzle.
-bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
-                  uint32_t box1);
+// multiple of 8); boxes of box1 rows of `swizzle_bytes` (32, 64 or 128), swizzled over that width.
+bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,
+                  int swizzle_bytes);
 
 // Four rows of a 2-D tensor (map box: one row) to four consecutive rows of
 // shared memory.  A row index past the tensor reads as zeros.

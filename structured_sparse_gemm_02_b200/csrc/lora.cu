@@ -191,32 +191,34 @@ struct Ring {
   uint64_t* full;
   uint64_t* empty;
   uint64_t* done;
-  uint64_t* aux;
+  uint64_t* more;  // eight further barriers (expand_kernel)
   uint32_t* tmem;
   volatile int* abort_flag;
 };
 constexpr int kMaxStages = 8;
-constexpr int kBarBytes = (2 * kMaxStages + 2) * 8 + 16;
+constexpr int kBarBytes = (2 * kMaxStages + 9) * 8 + 16;
 
 __device__ __forceinline__ Ring ring_at(uint8_t* p) {
   Ring r;
   r.full = reinterpret_cast<uint64_t*>(p);
   r.empty = r.full + kMaxStages;
   r.done = r.empty + kMaxStages;
-  r.aux = r.done + 1;
-  r.tmem = reinterpret_cast<uint32_t*>(r.aux + 1);
+  r.more = r.done + 1;
+  r.tmem = reinterpret_cast<uint32_t*>(r.more + 8);
   r.abort_flag = reinterpret_cast<volatile int*>(r.tmem + 1);
   return r;
 }
 
-__device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int warp) {
+// `readers` arrivals free a stage; `more`: arrivals of the further barriers.
+__device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int warp, int readers = 1,
+                                          const int* more = nullptr) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&r.full[s], 1);
-      mbar_init(&r.empty[s], 1);
+      mbar_init(&r.empty[s], readers);
     }
     mbar_init(r.done, 1);
-    mbar_init(r.aux, 1);
+    for (int i = 0; more && i < 8; ++i) mbar_init(&r.more[i], more[i]);
     *r.abort_flag = 0;
     fence_barrier_init();
   }
@@ -253,15 +255,78 @@ __device__ __forceinline__ uint64_t desc_mn_major(const void* p, uint32_t next64
   return smem_desc(smem_addr(p), next64, 1024, LAYOUT_SW128);
 }
 
-// Rows 4 lane .. 4 lane + 3 of a tile for one gather; positions past its end
-// name a row past the matrix, which reads as zeros.
-__device__ __forceinline__ int4 tile_rows(const int* perm, int pos, int count, int j, int M) {
-  int4 r;
-  r.x = j + 0 < count ? perm[pos + j + 0] : M;
-  r.y = j + 1 < count ? perm[pos + j + 1] : M;
-  r.z = j + 2 < count ? perm[pos + j + 2] : M;
-  r.w = j + 3 < count ? perm[pos + j + 3] : M;
-  return r;
+// The rows of a tile as a producer warp loads them, 32 at a time.  Consecutive
+// rows of the matrix (requests come as runs of rows) move as one box; others
+// are gathered four by four, which TMA does at about half the rate (shrink of
+// dY [8192, 16384] 118 us by gathers alone, 83 us with boxes).
+struct TileRows {
+  int4 rows;      // lane: positions 4 lane .. 4 lane + 3; a row past the matrix (zeros) past the end
+  unsigned runs;  // bit g: rows 32 g .. are consecutive
+  int count;
+};
+
+__device__ __forceinline__ TileRows tile_rows(const int* perm, int pos, int count, int lane, int M) {
+  TileRows t;
+  const int j = 4 * lane, first = j & ~31;
+  t.count = count;
+  t.rows.x = j + 0 < count ? perm[pos + j + 0] : M;
+  t.rows.y = j + 1 < count ? perm[pos + j + 1] : M;
+  t.rows.z = j + 2 < count ? perm[pos + j + 2] : M;
+  t.rows.w = j + 3 < count ? perm[pos + j + 3] : M;
+  const int want = __shfl_sync(0xffffffffu, t.rows.x, lane & ~7) + j - first;
+  const bool run = (j + 0 >= count || t.rows.x == want) && (j + 1 >= count || t.rows.y == want + 1) &&
+                   (j + 2 >= count || t.rows.z == want + 2) && (j + 3 >= count || t.rows.w == want + 3);
+  const unsigned lanes = __ballot_sync(0xffffffffu, run);
+  t.runs = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int n = count - 32 * g;
+    // ZERO-filled ends and short groups are gathered: a box would read past them
+    if (((lanes >> (8 * g)) & 0xFFu) == 0xFFu && n > 0) t.runs |= 1u << g;
+  }
+  return t;
+}
+
+// Loads 64 columns from x of the tile's rows (32 groups of `rowb` bytes a row)
+// to dst.  exact: only the tile's rows may be read as anything but zeros, as
+// where the row is summed over.  Returns the bytes to expect, the same on
+// every lane; `issue` false only counts.
+template <bool EXACT>
+__device__ __forceinline__ bool as_box(const TileRows& t, int g) {
+  const int n = t.count - 32 * g;
+  return (t.runs >> g & 1u) && (EXACT ? n >= 32 : n > 16);
+}
+template <bool EXACT>
+__device__ __forceinline__ uint32_t rows_bytes(const TileRows& t, int groups, uint32_t rowb) {
+  uint32_t b = 0;
+  for (int g = 0; g < groups; ++g) {
+    const int n = t.count - 32 * g;
+    if (as_box<EXACT>(t, g)) b += 32 * rowb;
+    else if (EXACT) b += 32 * rowb;
+    else if (n > 0) b += uint32_t((n < 32 ? n + 3 : 32) / 4) * 4 * rowb;
+  }
+  return b;
+}
+template <bool EXACT>
+__device__ __forceinline__ void rows_load(const TileRows& t, int groups, uint32_t rowb, uint8_t* dst,
+                                          const CUtensorMap* box, const CUtensorMap* one, int x, uint64_t* bar,
+                                          int lane) {
+  const int g = lane >> 3;
+  const int n = t.count - 32 * g;
+  if (g < groups) {
+    if (as_box<EXACT>(t, g)) {
+      if ((lane & 7) == 0) tma_load_2d(dst + g * 32 * rowb, box, x, t.rows.x, bar);
+    } else if (EXACT || 4 * (lane & 7) < n) {
+      tma_gather4(dst + lane * 4 * rowb, one, x, t.rows, bar);
+    }
+  }
+}
+
+// Layout of a K-major operand whose rows hold R elements: rows of 32, 64 or
+// 128 bytes (two tiles of 128 where R > 64), swizzled over their own width.
+__host__ __device__ inline int row_bytes_of(int R) { return R <= 16 ? 32 : R <= 32 ? 64 : 128; }
+__device__ __forceinline__ uint64_t desc_rows(const void* p, int rowb, uint32_t next) {
+  return smem_desc(smem_addr(p), next, 8 * rowb, rowb == 32 ? LAYOUT_SW32 : rowb == 64 ? LAYOUT_SW64 : LAYOUT_SW128);
 }
 
 // ---- shrink: P [rows][R] = T [rows][D] . G^T ----------------------------------------
@@ -269,19 +334,20 @@ __device__ __forceinline__ int4 tile_rows(const int* perm, int pos, int count, i
 // parts in tensor memory and add them through distributed shared memory in
 // the order of the ranks.  Warp 0 gathers T rows and loads G, one thread of
 // warp 1 issues the MMAs, all four warps read the accumulators.
-//   GMN false: G = A_l [R][D], a [64][R rows] box, K-major
-//   GMN true:  G = B_l [D][R], boxes of 64 rows x 64 columns, N-major
+//   GMN false: G = A_l [R][D], a box of R rows of 64 columns, K-major
+//   GMN true:  G = B_l [D][R], a box of 64 rows (two where R > 64), N-major
 struct ShrinkArgs {
   Plan plan;
   const float* scale;  // nullptr: 1
   void* P;
   int64_t ldp;
-  int M, D, R, stages, gbytes;
+  int M, D, R, stages, gbytes, rowb;
   uint32_t* err;
 };
 
 template <bool BF16, bool GMN>
 __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUtensorMap tmT,
+                                                     const __grid_constant__ CUtensorMap tmT1,
                                                      const __grid_constant__ CUtensorMap tmG, const ShrinkArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -310,9 +376,8 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
   const int kb0 = int(int64_t(nkb) * rank / cs), n = int(int64_t(nkb) * (rank + 1) / cs) - kb0;
 
   if (warp == 0) {
-    const int groups = (count + 3) / 4;
-    const int4 rows = tile_rows(a.plan.perm, pos, count, 4 * lane, a.M);
-    const uint32_t tx = groups * 512 + a.gbytes;
+    const TileRows rows = tile_rows(a.plan.perm, pos, count, lane, a.M);
+    const uint32_t tx = rows_bytes<false>(rows, 4, 128) + a.gbytes;
     int i = 0;
     for (; i < n; ++i) {
       const int s = i % a.stages;
@@ -322,7 +387,7 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
       const int k = (kb0 + i) * 64;
       if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], tx);
       __syncwarp();
-      if (lane < groups) tma_gather4(st + lane * 512, &tmT, k, rows, &ring.full[s]);
+      rows_load<false>(rows, 4, 128, st, &tmT, &tmT1, k, &ring.full[s], lane);
       if (lane == 0) {
         if constexpr (GMN) {
           tma_load_3d(st + kTile * 128, &tmG, 0, k, adapter, &ring.full[s]);
@@ -345,10 +410,10 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
         tc_fence_after();
         uint8_t* st = smem + s * stage_bytes;
         const uint64_t ad = desc_k_major(st);
-        const uint64_t bd = GMN ? desc_mn_major(st + kTile * 128, 8192) : desc_k_major(st + kTile * 128);
+        const uint64_t bd = GMN ? desc_rows(st + kTile * 128, a.rowb, 8192) : desc_k_major(st + kTile * 128);
+        const int bstep = (GMN ? 16 * a.rowb : 32) >> 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma(tmem, ad + ((32 * k) >> 4), bd + ((GMN ? 2048 * k : 32 * k) >> 4), idesc, (i | k) != 0);
+        for (int k = 0; k < 4; ++k) tc_mma(tmem, ad + ((32 * k) >> 4), bd + k * bstep, idesc, (i | k) != 0);
         tc_commit(&ring.empty[s]);
       }
       tc_commit(ring.done);
@@ -403,9 +468,16 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
 }
 
 // ---- expand: Y [rows][C] = base + s P [rows][R] . G^T ---------------------------------
-// One block a tile and 128 columns.  The rows of base come in by bulk copies
-// (one a row) while the MMA runs, the sum is rounded in place and goes out the
-// same way; the columns behind the last multiple of 8 move element by element.
+// A block of work is a tile and 128 columns; each SM's block takes an equal,
+// consecutive share of them all and keeps the loads of the next ones under
+// way (one block a tile and 128 columns, started anew each time, took 165 us
+// for [8192, 16384] where this one's traffic takes 82).
+//   warp 0    producer: base and G of the next blocks into the ring, P of the
+//             next tile into one of two slots
+//   warp 1    MMAs (one thread), tensor memory
+//   warps 2-9 two a quarter of the rows, 64 columns each: accumulator + base
+//             from the ring, rounded in place and stored from there (a box
+//             where the rows are consecutive, else coalesced stores)
 //   GMN false: G = B_l [C][R];  GMN true: G = A_l [R][C]
 struct ExpandArgs {
   Plan plan;
@@ -413,147 +485,281 @@ struct ExpandArgs {
   const void* base;    // nullptr: 0
   void* Y;
   int64_t ldb, ldy;
-  int M, C, R;
+  int M, C, R, stages, rowb, pbytes, gbytes;
   uint32_t* err;
 };
 
 constexpr int kExpCols = 128;
-constexpr int kExpPitch = kExpCols * 2 + 16;  // bytes of a staged row: 16-byte accesses of eight lanes miss each other
+constexpr int kExpThreads = 320;
+constexpr int kYBytes = kTile * kExpCols * 2;
+
+// The consecutive share of the blocks of work that this thread block takes,
+// one by one: column block nb of tile `tile`.
+struct Share {
+  int left, tile, nb, nblk;
+  bool fresh;  // the first block of its tile here
+  __device__ Share(int tiles, int nblk_) : nblk(nblk_), fresh(true) {
+    const int64_t total = int64_t(tiles) * nblk_;
+    const int64_t w = total * blockIdx.x / gridDim.x;
+    left = int(total * (blockIdx.x + 1) / gridDim.x - w);
+    tile = int(w / nblk_);
+    nb = int(w - int64_t(tile) * nblk_);
+  }
+  __device__ bool more() const { return left > 0; }
+  __device__ bool last_of_tile() const { return left == 1 || nb + 1 == nblk; }
+  __device__ void next() {
+    --left;
+    fresh = false;
+    if (++nb == nblk) {
+      nb = 0;
+      ++tile;
+      fresh = true;
+    }
+  }
+};
 
 template <bool BF16, bool GMN>
-__global__ void __launch_bounds__(128) expand_kernel(const __grid_constant__ CUtensorMap tmP,
-                                                     const __grid_constant__ CUtensorMap tmG, const ExpandArgs a) {
+__global__ void __launch_bounds__(kExpThreads, 1)
+    expand_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmG,
+                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB1,
+                  const __grid_constant__ CUtensorMap tmY, const ExpandArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stage_bytes = kYBytes + a.gbytes;
+  uint8_t* Ps = smem + a.stages * stage_bytes;  // two slots
+  const Ring ring = ring_at(Ps + 2 * a.pbytes);
+  uint64_t* acc_full = ring.more;       // two accumulators
+  uint64_t* acc_empty = ring.more + 2;
+  uint64_t* p_full = ring.more + 4;     // two slots of P
+  uint64_t* p_empty = ring.more + 6;
+  const int counts[8] = {1, 1, 8, 8, 1, 1, 1, 1};
   griddep_wait();
-  if (int(blockIdx.y) >= a.plan.hdr[0]) return;
-  const int4 t = a.plan.tiles[blockIdx.y];
-  const int adapter = t.x, pos = t.y, count = t.z;
-  const int n0 = blockIdx.x * kExpCols;
-  const int cols = min(kExpCols, a.C - n0);
-  const bool live = int(threadIdx.x) < count;
-  const int64_t row = live ? a.plan.perm[pos + threadIdx.x] : 0;
-  const uint16_t* base = static_cast<const uint16_t*>(a.base);
-  uint16_t* Y = static_cast<uint16_t*>(a.Y);
-  if (adapter < 0) {  // rows without an adapter: base as it is
-    if (base == Y) return;
-    for (int r = warp; r < count; r += 4) {
-      const int64_t from = a.plan.perm[pos + r];
-      for (int c = lane * 4; c < cols; c += 128) {
-        uint16_t* o = Y + from * a.ldy + n0 + c;
-        const uint16_t* b = base + from * a.ldb + n0 + c;
-        if (c + 4 <= cols)
-          *reinterpret_cast<uint2*>(o) = base ? *reinterpret_cast<const uint2*>(b) : make_uint2(0u, 0u);
-        else
-          for (int e = 0; e < cols - c; ++e) o[e] = base ? b[e] : uint16_t(0);
-      }
-    }
-    return;
-  }
-  const int Rn = round16(a.R);
-  const int halves = a.R > 64 ? 2 : 1;
-  uint8_t* Ps = smem;
-  uint8_t* Gs = Ps + halves * kTile * 128;
-  const int gbytes = GMN ? 2 * Rn * 128 : halves * kExpCols * 128;
-  uint8_t* Ys = Gs + gbytes;
-  const Ring ring = ring_at(Ys + kTile * kExpPitch);
-  ring_init(ring, kExpCols, warp);
+  ring_init(ring, 2 * kExpCols, warp, 8, counts);
   const uint32_t tmem = *ring.tmem;
-  const int bulk = cols / 8 * 8;  // columns that move in 16-byte pieces
-  uint8_t* mine = Ys + threadIdx.x * kExpPitch;
+  const int halves = a.R > 64 ? 2 : 1;
+  const int Rn = round16(a.R);
+  Share w(a.plan.hdr[0], (a.C + kExpCols - 1) / kExpCols);
+  const bool has_base = a.base != nullptr;
+  const bool in_place = a.base == a.Y;
+  // Every role walks the same blocks: i counts those that are not skipped
+  // (rows without an adapter whose base is already in place), p those tiles
+  // that need a slot of P.
   if (warp == 0) {
-    const int groups = (count + 3) / 4;
-    const int4 rows = tile_rows(a.plan.perm, pos, count, 4 * lane, a.M);
-    if (lane == 0) {
-      if (base && bulk) mbar_arrive_expect_tx(ring.aux, uint32_t(count) * bulk * 2);
-      mbar_arrive_expect_tx(&ring.full[0], halves * groups * 512 + gbytes);
-    }
-    __syncwarp();
-    for (int h = 0; h < halves; ++h)
-      if (lane < groups) tma_gather4(Ps + h * kTile * 128 + lane * 512, &tmP, 64 * h, rows, &ring.full[0]);
-    if (lane == 0) {
-      if constexpr (GMN) {
-        tma_load_3d(Gs, &tmG, n0, 0, adapter, &ring.full[0]);
-        tma_load_3d(Gs + Rn * 128, &tmG, n0 + 64, 0, adapter, &ring.full[0]);
-      } else {
-        for (int h = 0; h < halves; ++h)
-          tma_load_3d(Gs + h * kExpCols * 128, &tmG, 64 * h, n0, adapter, &ring.full[0]);
+    int i = 0, p = 0;
+    int4 t = make_int4(-1, 0, 0, 0);
+    TileRows rows;
+    uint32_t bytes = 0;
+    for (; w.more(); w.next()) {
+      const int n0 = w.nb * kExpCols;
+      if (w.fresh) {
+        t = a.plan.tiles[w.tile];
+        rows = tile_rows(a.plan.perm, t.y, t.z, lane, a.M);
+        bytes = rows_bytes<false>(rows, 4, 128);
       }
+      if (t.x < 0 && in_place) continue;
+      if (w.fresh && t.x >= 0) {
+        const int slot = p & 1;
+        if (p >= 2 && !mbar_wait_warp(&p_empty[slot], ((p >> 1) - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
+        const int fours = (t.z + 3) / 4;
+        if (lane == 0) mbar_arrive_expect_tx(&p_full[slot], halves * fours * 4 * a.rowb);
+        __syncwarp();
+        for (int h = 0; h < halves; ++h)
+          if (lane < fours)
+            tma_gather4(Ps + slot * a.pbytes + h * kTile * a.rowb + lane * 4 * a.rowb, &tmP, 64 * h, rows.rows,
+                        &p_full[slot]);
+        ++p;
+      }
+      const int s = i % a.stages;
+      const int use = i / a.stages;
+      if (use > 0 && !mbar_wait_warp(&ring.empty[s], (use - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
+      uint8_t* st = smem + s * stage_bytes;
+      const int subs = a.C - n0 > 64 ? 2 : 1;
+      if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], (has_base ? subs * bytes : 0u) + (t.x >= 0 ? a.gbytes : 0));
+      __syncwarp();
+      if (has_base)
+        for (int j = 0; j < subs; ++j)
+          rows_load<false>(rows, 4, 128, st + j * kTile * 128, &tmB, &tmB1, n0 + 64 * j, &ring.full[s], lane);
+      if (t.x >= 0 && lane == 0) {
+        uint8_t* g = st + kYBytes;
+        if constexpr (GMN) {
+          tma_load_3d(g, &tmG, n0, 0, t.x, &ring.full[s]);
+          tma_load_3d(g + Rn * 128, &tmG, n0 + 64, 0, t.x, &ring.full[s]);
+        } else {
+          for (int h = 0; h < halves; ++h)
+            tma_load_3d(g + h * kExpCols * a.rowb, &tmG, 64 * h, n0, t.x, &ring.full[s]);
+        }
+      }
+      __syncwarp();
+      ++i;
     }
-    __syncwarp();
-  }
-  if (base && bulk && live) bulk_load(smem_addr(mine), base + row * a.ldb + n0, bulk * 2, ring.aux);
-  if (warp == 1) {
+    if (lane == 0) {  // nothing is in flight when the block ends
+      for (int q = i > a.stages ? i - a.stages : 0; q < i; ++q)
+        tail_wait(&ring.full[q % a.stages], (q / a.stages) & 1, a.err);
+      for (int q = p > 2 ? p - 2 : 0; q < p; ++q) tail_wait(&p_full[q & 1], (q >> 1) & 1, a.err);
+    }
+  } else if (warp == 1) {
     if (lane == 0) {
-      tail_wait(&ring.full[0], 0, a.err);
-      tc_fence_after();
       const uint32_t idesc = instr_desc_major(BF16, kTile, kExpCols, 0, GMN ? 1 : 0);
-      for (int k = 0; k < Rn / 16; ++k) {
-        const uint64_t ad = desc_k_major(Ps + (k >> 2) * kTile * 128) + ((32 * (k & 3)) >> 4);
-        const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, Rn * 128)
-                                : desc_k_major(Gs + (k >> 2) * kExpCols * 128) + ((32 * (k & 3)) >> 4);
-        tc_mma(tmem, ad, bd, idesc, k != 0);
+      int i = 0, p = 0, adapter = -1;
+      for (; w.more(); w.next()) {
+        if (w.fresh) adapter = a.plan.tiles[w.tile].x;
+        if (adapter < 0 && in_place) continue;
+        if (w.fresh && adapter >= 0) {
+          if (!mbar_wait(&p_full[p & 1], (p >> 1) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
+          ++p;
+        }
+        const int s = i % a.stages, b = i & 1;
+        if (!mbar_wait(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
+        if (i >= 2 && !mbar_wait(&acc_empty[b], ((i >> 1) - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC_FREE)) break;
+        tc_fence_after();
+        if (adapter >= 0) {
+          const uint8_t* P = Ps + ((p - 1) & 1) * a.pbytes;
+          const uint8_t* G = smem + s * stage_bytes + kYBytes;
+          const int ksub = a.rowb / 32;  // MMA steps in a row of an operand tile
+          for (int k = 0; k < Rn / 16; ++k) {
+            const int h = k / ksub, kk = k - h * ksub;
+            const uint64_t ad = desc_rows(P + h * kTile * a.rowb, a.rowb, 16) + ((32 * kk) >> 4);
+            const uint64_t bd = GMN ? desc_mn_major(G + 2048 * k, Rn * 128)
+                                    : desc_rows(G + h * kExpCols * a.rowb, a.rowb, 16) + ((32 * kk) >> 4);
+            tc_mma(tmem + b * kExpCols, ad, bd, idesc, k != 0);
+          }
+          if (w.last_of_tile()) tc_commit(&p_empty[(p - 1) & 1]);
+        }
+        tc_commit(&acc_full[b]);
+        ++i;
       }
       tc_commit(ring.done);
     }
     __syncwarp();
-  }
-  const float scale = a.scale ? a.scale[adapter] : 1.f;
-  tail_wait(ring.done, 0, a.err);
-  if (base && bulk) tail_wait(ring.aux, 0, a.err);
-  __syncwarp();
-  tc_fence_after();
-  if (32 * warp < count) {
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-      uint32_t h[32];
-      tmem_ld_32x32b_x32(tmem + (uint32_t(32 * warp) << 16) + c, h);
-      tmem_ld_wait(h);
-      if (live) {
+    tail_wait(ring.done, 0, a.err);
+  } else {
+    const int quad = warp & 3, sub = (warp - 2) >> 2;
+    uint16_t* Y = static_cast<uint16_t*>(a.Y);
+    int i = 0, pending = -1;
+    int4 t = make_int4(-1, 0, 0, 0);
+    int mine = 0;       // this lane's row
+    bool run = false;   // the warp's 32 rows are consecutive, and all there
+    int rows_here = 0;
+    float scale = 0.f;
+    for (; w.more(); w.next()) {
+      const int n0 = w.nb * kExpCols + 64 * sub;
+      if (w.fresh) {
+        t = a.plan.tiles[w.tile];
+        rows_here = t.z - 32 * quad;
+        mine = lane < rows_here ? a.plan.perm[t.y + 32 * quad + lane] : 0;
+        const int first = __shfl_sync(0xffffffffu, mine, 0);
+        run = rows_here >= 32 && __all_sync(0xffffffffu, mine == first + lane);
+        scale = t.x < 0 ? 0.f : a.scale ? a.scale[t.x] : 1.f;
+      }
+      if (t.x < 0 && in_place) continue;
+      const int s = i % a.stages, b = i & 1;
+      // the copied rows' own barrier, then the accumulator's
+      bool ok = mbar_wait_warp(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC);
+      ok = ok && mbar_wait_warp(&acc_full[b], (i >> 1) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC);
+      if (!ok) break;
+      tc_fence_after();
+      const int cols = min(64, a.C - n0);
+      uint8_t* buf = smem + s * stage_bytes + sub * kTile * 128 + quad * 32 * 128;
+      bool boxed = false;
+      if (rows_here > 0 && cols > 0) {
+        uint8_t* row = buf + lane * 128;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int at = c + 8 * v;
-          if (at + 8 <= cols) {
-            uint4 b = make_uint4(0u, 0u, 0u, 0u);
-            if (base) b = *reinterpret_cast<const uint4*>(mine + at * 2);
-            uint32_t* bw = reinterpret_cast<uint32_t*>(&b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack2<BF16>(bw[e]);
-              bw[e] = pack2<BF16>(fmaf(scale, __uint_as_float(h[8 * v + 2 * e]), f.x),
-                                  fmaf(scale, __uint_as_float(h[8 * v + 2 * e + 1]), f.y));
-            }
-            *reinterpret_cast<uint4*>(mine + at * 2) = b;
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t h[32];
+          if (t.x >= 0) {
+            tmem_ld_32x32b_x32(tmem + (uint32_t(32 * quad) << 16) + b * kExpCols + 64 * sub + c, h);
+            tmem_ld_wait(h);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (at + e < cols) {
-                const float f = base ? unpack1<BF16>(base[row * a.ldb + n0 + at + e]) : 0.f;
-                Y[row * a.ldy + n0 + at + e] = pack1<BF16>(fmaf(scale, __uint_as_float(h[8 * v + e]), f));
+            for (int e = 0; e < 32; ++e) h[e] = 0u;
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            // 16-byte piece v of the row's 64 columns, where the swizzle puts it
+            uint4* at = reinterpret_cast<uint4*>(row + (((c / 8 + v) ^ (lane & 7)) << 4));
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (has_base) x = *at;
+            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+            if (t.x >= 0) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<BF16>(xw[e]);
+                xw[e] = pack2<BF16>(fmaf(scale, __uint_as_float(h[8 * v + 2 * e]), f.x),
+                                    fmaf(scale, __uint_as_float(h[8 * v + 2 * e + 1]), f.y));
               }
+            }
+            *at = x;
           }
         }
+        boxed = run && cols == 64;
+        if (boxed) {
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
       }
+      tc_fence_before();
       __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+      if (boxed) {
+        if (lane == 0) {
+          tma_store_2d_saddr(&tmY, smem_addr(buf), n0, mine);
+          bulk_commit();
+          // the stage of the store before this one, once that has left shared memory
+          if (pending >= 0) {
+            bulk_wait_read<1>();
+            mbar_arrive(&ring.empty[pending]);
+          }
+        }
+        pending = s;
+      } else {
+        if (rows_here > 0 && cols > 0) {
+          // eight lanes a row, four rows at a time
+          for (int r = 0; r < 32; r += 4) {
+            const int rr = r + (lane >> 3), c = (lane & 7) * 8;
+            const int64_t to = __shfl_sync(0xffffffffu, mine, rr);
+            if (rr < rows_here && c < cols) {
+              const uint4 x = *reinterpret_cast<const uint4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+              uint16_t* o = Y + to * a.ldy + n0 + c;
+              if (c + 8 <= cols) {
+                *reinterpret_cast<uint4*>(o) = x;
+              } else {
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                  if (c + e < cols) o[e] = static_cast<uint16_t>(xw[e >> 1] >> (16 * (e & 1)));
+              }
+            }
+          }
+        }
+        // generic reads of the stage come before the copies that refill it
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (pending >= 0) {
+            bulk_wait_read<0>();
+            mbar_arrive(&ring.empty[pending]);
+          }
+          mbar_arrive(&ring.empty[s]);
+        }
+        pending = -1;
+      }
+      ++i;
     }
+    if (lane == 0) bulk_wait_all<0>();
+    __syncwarp();
   }
+  __syncwarp();
   tc_fence_before();
-  if (live && bulk) {
-    fence_proxy_async_smem();
-    bulk_store(Y + row * a.ldy + n0, smem_addr(mine), bulk * 2);
-    bulk_commit();
-    bulk_wait_all<0>();
-  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kExpCols);
+    tmem_dealloc(tmem, 2 * kExpCols);
   }
 }
 
 // ---- wgrad: dG_l [C][R] = s_l sum over l's rows of T[m][c] P[m][r] ----------------------
-// One cluster a block of 256 columns of T and an adapter; its blocks split
+// One cluster a block of kWgCols columns of T and an adapter; its blocks split
 // the adapter's rows in chunks of 64 and add their sums as shrink_kernel does.
 // Both operands are read with the row as the MMA's K index.
 //   OT false: dG is [C][R] (dB);  OT true: [R][C] (dA)
@@ -561,15 +767,17 @@ struct WgradArgs {
   Plan plan;
   const float* scale;  // nullptr: 1
   void* dG;
-  int M, C, R, stages;
+  int M, C, R, stages, rowb;
   uint32_t* err;
 };
 
-constexpr int kWgCols = 256;
+constexpr int kWgCols = 128;
 
 template <bool BF16, bool OT>
 __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUtensorMap tmT,
-                                                    const __grid_constant__ CUtensorMap tmP, const WgradArgs a) {
+                                                    const __grid_constant__ CUtensorMap tmT1,
+                                                    const __grid_constant__ CUtensorMap tmP,
+                                                    const __grid_constant__ CUtensorMap tmP1, const WgradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -597,33 +805,33 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
   const int Rn = round16(R), halves = R > 64 ? 2 : 1;
   const int subs = (cols + 63) / 64;  // tiles of 64 columns inside the matrix
   const int tbytes = (kWgCols / 64) * 8192;
-  const int stage_bytes = tbytes + halves * 8192;
+  const int pbytes = 64 * a.rowb;
+  const int stage_bytes = tbytes + halves * pbytes;
   const int part_bytes = kWgCols * (R + 4) * 4;
   const int ring_bytes = a.stages * stage_bytes;
   const Ring ring = ring_at(smem + (ring_bytes > part_bytes ? ring_bytes : part_bytes));
-  const uint32_t tcols = tmem_cols(2 * Rn);
+  const uint32_t tcols = tmem_cols(Rn);
   ring_init(ring, tcols, warp);
   const uint32_t tmem = *ring.tmem;
   const int chunks = (rows + 63) / 64;
   const int q0 = int(int64_t(chunks) * rank / cs), n = int(int64_t(chunks) * (rank + 1) / cs) - q0;
 
   if (warp == 0) {
-    const uint32_t tx = (subs + halves) * 8192;
-    const int group = lane & 15;
+    const uint32_t tx = subs * 8192 + halves * pbytes;
     int i = 0;
     for (; i < n; ++i) {
       const int s = i % a.stages;
       const uint32_t use = i / a.stages;
       const int at = (q0 + i) * 64;
-      const int4 r = tile_rows(a.plan.perm, start + at, rows - at, 4 * group, a.M);
+      const TileRows r = tile_rows(a.plan.perm, start + at, min(64, rows - at), lane, a.M);
       if (use > 0 && !mbar_wait_warp(&ring.empty[s], (use - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
       uint8_t* st = smem + s * stage_bytes;
       if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], tx);
       __syncwarp();
-      for (int j = lane >> 4; j < subs; j += 2)
-        tma_gather4(st + j * 8192 + group * 512, &tmT, c0 + 64 * j, r, &ring.full[s]);
-      if ((lane >> 4) < halves)
-        tma_gather4(st + tbytes + (lane >> 4) * 8192 + group * 512, &tmP, 64 * (lane >> 4), r, &ring.full[s]);
+      for (int j = 0; j < subs; ++j)
+        rows_load<true>(r, 2, 128, st + j * 8192, &tmT, &tmT1, c0 + 64 * j, &ring.full[s], lane);
+      for (int h = 0; h < halves; ++h)
+        rows_load<true>(r, 2, a.rowb, st + tbytes + h * pbytes, &tmP, &tmP1, 64 * h, &ring.full[s], lane);
       __syncwarp();
     }
     if (lane == 0)
@@ -637,13 +845,10 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
         if (!mbar_wait(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
         tc_fence_after();
         uint8_t* st = smem + s * stage_bytes;
-        const uint64_t bd = desc_mn_major(st + tbytes, 8192);
-        for (int h = 0; h < 2 && 128 * h < cols; ++h) {
-          const uint64_t ad = desc_mn_major(st + h * 16384, 8192);
+        const uint64_t ad = desc_mn_major(st, 8192), bd = desc_rows(st + tbytes, a.rowb, pbytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma(tmem + h * Rn, ad + ((2048 * k) >> 4), bd + ((2048 * k) >> 4), idesc, (i | k) != 0);
-        }
+        for (int k = 0; k < 4; ++k)
+          tc_mma(tmem, ad + ((2048 * k) >> 4), bd + ((16 * a.rowb * k) >> 4), idesc, (i | k) != 0);
         tc_commit(&ring.empty[s]);
       }
       tc_commit(ring.done);
@@ -657,15 +862,13 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
   const int pitch = R + 4;
   float* part = reinterpret_cast<float*>(smem);
   if (n > 0) {
-    for (int h = 0; h < 2 && 128 * h < cols; ++h) {
-      float* mine = part + (128 * h + 32 * warp + lane) * pitch;
-      for (int c = 0; c < R; c += 8) {
-        uint32_t r[8];
-        tmem_ld_32x32b_x8(tmem + (uint32_t(32 * warp) << 16) + h * Rn + c, r);
-        tmem_ld_wait(r);
-        *reinterpret_cast<uint4*>(mine + c) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(mine + c + 4) = make_uint4(r[4], r[5], r[6], r[7]);
-      }
+    float* mine = part + (32 * warp + lane) * pitch;
+    for (int c = 0; c < R; c += 8) {
+      uint32_t r[8];
+      tmem_ld_32x32b_x8(tmem + (uint32_t(32 * warp) << 16) + c, r);
+      tmem_ld_wait(r);
+      *reinterpret_cast<uint4*>(mine + c) = make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4*>(mine + c + 4) = make_uint4(r[4], r[5], r[6], r[7]);
     }
   }
   __syncwarp();
@@ -713,44 +916,45 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
 }
 
 // ---- host ---------------------------------------------------------------------------
-// Shared-memory budget of a ring: two blocks an SM.
-constexpr int kRingBudget = 100 * 1024;
-
 template <class K>
 spg_status prepare(K kern, int smem) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? SPG_OK
                                                                                                       : SPG_ERR_CUDA;
 }
 
-// T rows for gathers: boxes of one row of 64 columns.
-bool rows_map(CUtensorMap* m, const void* p, int64_t cols, int64_t rows, int64_t ld) {
-  return make_tmap_2d(m, p, 2, uint64_t(cols), uint64_t(rows), uint64_t(ld) * 2, 64, 1, true);
+// Rows of a matrix: boxes of 32 rows, and single rows for gathers, of `rowb` bytes.
+bool rows_maps(CUtensorMap* box, CUtensorMap* one, const void* p, int64_t cols, int64_t rows, int64_t ld, int rowb) {
+  return make_tmap_2d_swz(box, p, 2, uint64_t(cols), uint64_t(rows), uint64_t(ld) * 2, rowb / 2, 32, rowb) &&
+         make_tmap_2d_swz(one, p, 2, uint64_t(cols), uint64_t(rows), uint64_t(ld) * 2, rowb / 2, 1, rowb);
 }
+
+constexpr int kRingBudget = 100 * 1024;  // shared memory of a ring where two blocks share an SM
 
 template <bool BF16, bool GMN>
 spg_status shrink(const void* T, int64_t ldt, const void* G, const float* scale, const Plan& plan, void* P, int64_t ldp,
                   int64_t M, int64_t D, int64_t R, int64_t L, uint32_t* err, cudaStream_t st) {
-  const int Rn = round16(int(R));
-  CUtensorMap tmT, tmG;
-  if (!rows_map(&tmT, T, D, M, ldt)) return SPG_ERR_CUDA;
-  if (!(GMN ? make_tmap_3d(&tmG, G, R, D, L, 64, 64) : make_tmap_3d(&tmG, G, D, R, L, 64, Rn))) return SPG_ERR_CUDA;
-  const int gbytes = GMN ? (R > 64 ? 16384 : 8192) : Rn * 128;
+  const int Rn = round16(int(R)), rowb = row_bytes_of(int(R));
+  CUtensorMap tmT, tmT1, tmG;
+  if (!rows_maps(&tmT, &tmT1, T, D, M, ldt, 128)) return SPG_ERR_CUDA;
+  if (!(GMN ? make_tmap_3d(&tmG, G, R, D, L, 64, rowb) : make_tmap_3d(&tmG, G, D, R, L, Rn, 128))) return SPG_ERR_CUDA;
+  const int gbytes = GMN ? 64 * rowb * (R > 64 ? 2 : 1) : Rn * 128;
   const int stage = kTile * 128 + gbytes;
   int stages = kRingBudget / stage;
   stages = stages > kMaxStages ? kMaxStages : stages;
-  // blocks of a cluster: enough to fill the device with the tiles of full
-  // groups, each with at least two steps of its own
+  // blocks of a cluster: as many as let every tile of full groups be resident
+  // at once (two blocks an SM), each with at least two steps of its own
   const int64_t tiles = max_tiles(M, L), nkb = (D + 63) / 64;
   const int64_t busy = (M + kTile - 1) / kTile;
   int cs = 1;
-  while (cs < 8 && busy * cs < 2 * sm_count() && nkb >= 4 * cs) cs *= 2;
+  while (cs < 8 && busy * 2 * cs <= 2 * sm_count() && nkb >= 4 * cs) cs *= 2;
   const int ring = stages * stage, part = kTile * (int(R) + 4) * 4;
+  const int smem = (ring > part ? ring : part) + kBarBytes + 1024;
   if (part > ring) return SPG_ERR_UNSUPPORTED_SHAPE;
-  const int smem = ring + kBarBytes + 1024;
   auto kern = shrink_kernel<BF16, GMN>;
   if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const ShrinkArgs a{plan, scale, P, ldp, int(M), int(D), int(R), stages, gbytes, err};
-  return launch_pdl_cluster(kern, dim3(unsigned(tiles * cs)), dim3(128), smem, cs, st, tmT, tmG, a) == cudaSuccess
+  const ShrinkArgs a{plan, scale, P, ldp, int(M), int(D), int(R), stages, gbytes, rowb, err};
+  return launch_pdl_cluster(kern, dim3(unsigned(tiles * cs)), dim3(128), smem, cs, st, tmT, tmT1, tmG, a) ==
+                 cudaSuccess
              ? launch_status()
              : SPG_ERR_CUDA;
 }
@@ -759,38 +963,50 @@ template <bool BF16, bool GMN>
 spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale, const Plan& plan, const void* base,
                   int64_t ldb, void* Y, int64_t ldy, int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err,
                   cudaStream_t st) {
-  const int Rn = round16(int(R)), halves = R > 64 ? 2 : 1;
-  CUtensorMap tmP, tmG;
-  if (!rows_map(&tmP, P, R, M, ldp)) return SPG_ERR_CUDA;
-  if (!(GMN ? make_tmap_3d(&tmG, G, C, R, L, 64, Rn) : make_tmap_3d(&tmG, G, R, C, L, 64, kExpCols)))
+  const int Rn = round16(int(R)), halves = R > 64 ? 2 : 1, rowb = row_bytes_of(int(R));
+  CUtensorMap tmP, tmP32, tmG, tmB, tmB1, tmY, tmY1;
+  if (!rows_maps(&tmP32, &tmP, P, R, M, ldp, rowb) || !rows_maps(&tmY, &tmY1, Y, C, M, ldy, 128) ||
+      !rows_maps(&tmB, &tmB1, base ? base : Y, C, M, base ? ldb : ldy, 128))
     return SPG_ERR_CUDA;
-  const int smem = halves * kTile * 128 + (GMN ? 2 * Rn * 128 : halves * kExpCols * 128) + kTile * kExpPitch +
-                   kBarBytes + 1024;
+  if (!(GMN ? make_tmap_3d(&tmG, G, C, R, L, Rn, 128) : make_tmap_3d(&tmG, G, R, C, L, kExpCols, rowb)))
+    return SPG_ERR_CUDA;
+  const int pbytes = halves * kTile * rowb;
+  const int gbytes = GMN ? 2 * Rn * 128 : halves * kExpCols * rowb;
+  const int fixed = 2 * pbytes + kBarBytes + 1024;
+  int stages = (232448 - fixed) / (kYBytes + gbytes);
+  stages = stages > kMaxStages ? kMaxStages : stages;
+  const int smem = stages * (kYBytes + gbytes) + fixed;
   auto kern = expand_kernel<BF16, GMN>;
   if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const ExpandArgs a{plan, scale, base, Y, ldb, ldy, int(M), int(C), int(R), err};
-  const dim3 grid(unsigned((C + kExpCols - 1) / kExpCols), unsigned(max_tiles(M, L)));
-  return launch_pdl(kern, grid, dim3(128), smem, st, tmP, tmG, a) == cudaSuccess ? launch_status() : SPG_ERR_CUDA;
+  const ExpandArgs a{plan, scale, base, Y, ldb, ldy, int(M), int(C), int(R), stages, rowb, pbytes, gbytes, err};
+  const int64_t work = max_tiles(M, L) * ((C + kExpCols - 1) / kExpCols);
+  const int64_t blocks = work < sm_count() ? work : sm_count();
+  return launch_pdl(kern, dim3(unsigned(blocks)), dim3(kExpThreads), smem, st, tmP, tmG, tmB, tmB1, tmY, a) ==
+                 cudaSuccess
+             ? launch_status()
+             : SPG_ERR_CUDA;
 }
 
 template <bool BF16, bool OT>
 spg_status wgrad(const void* T, int64_t ldt, const void* P, int64_t ldp, const float* scale, const Plan& plan, void* dG,
                  int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err, cudaStream_t st) {
-  CUtensorMap tmT, tmP;
-  if (!rows_map(&tmT, T, C, M, ldt) || !rows_map(&tmP, P, R, M, ldp)) return SPG_ERR_CUDA;
-  const int stage = (kWgCols / 64 + (R > 64 ? 2 : 1)) * 8192;
-  const int stages = 204800 / stage;
+  const int rowb = row_bytes_of(int(R));
+  CUtensorMap tmT, tmT1, tmP, tmP1;
+  if (!rows_maps(&tmT, &tmT1, T, C, M, ldt, 128) || !rows_maps(&tmP, &tmP1, P, R, M, ldp, rowb)) return SPG_ERR_CUDA;
+  const int stage = (kWgCols / 64) * 8192 + (R > 64 ? 2 : 1) * 64 * rowb;
+  int stages = kRingBudget / stage;
+  stages = stages > kMaxStages ? kMaxStages : stages;
   const int64_t blocks = (C + kWgCols - 1) / kWgCols;
   const int64_t groups = L < 4 ? L : 4;
   int cs = 1;
-  while (cs < 8 && blocks * groups * cs < 2 * sm_count() && M / groups >= 128 * cs) cs *= 2;
+  while (cs < 8 && blocks * groups * cs < 4 * sm_count() && M / groups >= 256 * cs) cs *= 2;
   const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
   const int smem = (ring > part ? ring : part) + kBarBytes + 1024;
   auto kern = wgrad_kernel<BF16, OT>;
   if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const WgradArgs a{plan, scale, dG, int(M), int(C), int(R), stages, err};
-  return launch_pdl_cluster(kern, dim3(unsigned(blocks * cs), unsigned(L)), dim3(128), smem, cs, st, tmT, tmP, a) ==
-                 cudaSuccess
+  const WgradArgs a{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
+  return launch_pdl_cluster(kern, dim3(unsigned(blocks * cs), unsigned(L)), dim3(128), smem, cs, st, tmT, tmT1, tmP,
+                            tmP1, a) == cudaSuccess
              ? launch_status()
              : SPG_ERR_CUDA;
 }
