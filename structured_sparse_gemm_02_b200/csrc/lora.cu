@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gather.cuh"
 #include "host.cuh"
@@ -191,12 +192,26 @@ struct Ring {
   uint64_t* full;
   uint64_t* empty;
   uint64_t* done;
-  uint64_t* more;  // eight further barriers (expand_kernel)
+  uint64_t* more;  // twelve further barriers (expand_kernel)
   uint32_t* tmem;
   volatile int* abort_flag;
 };
+// A role's place in a ring of n: slot and the parity of its use of the slot
+// (kept, as a division a step costs a single thread more than the step).  A
+// fresh barrier passes a wait for parity 1.
+struct Turn {
+  int n, s = 0;
+  uint32_t ph = 0;
+  __device__ explicit Turn(int n_) : n(n_) {}
+  __device__ __forceinline__ void next() {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
 constexpr int kMaxStages = 8;
-constexpr int kBarBytes = (2 * kMaxStages + 9) * 8 + 16;
+constexpr int kBarBytes = (2 * kMaxStages + 13) * 8 + 16;
 
 __device__ __forceinline__ Ring ring_at(uint8_t* p) {
   Ring r;
@@ -204,7 +219,7 @@ __device__ __forceinline__ Ring ring_at(uint8_t* p) {
   r.empty = r.full + kMaxStages;
   r.done = r.empty + kMaxStages;
   r.more = r.done + 1;
-  r.tmem = reinterpret_cast<uint32_t*>(r.more + 8);
+  r.tmem = reinterpret_cast<uint32_t*>(r.more + 12);
   r.abort_flag = reinterpret_cast<volatile int*>(r.tmem + 1);
   return r;
 }
@@ -218,7 +233,7 @@ __device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int
       mbar_init(&r.empty[s], readers);
     }
     mbar_init(r.done, 1);
-    for (int i = 0; more && i < 8; ++i) mbar_init(&r.more[i], more[i]);
+    for (int i = 0; more && i < 12; ++i) mbar_init(&r.more[i], more[i]);
     *r.abort_flag = 0;
     fence_barrier_init();
   }
@@ -230,8 +245,8 @@ __device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Only now: a dependent kernel that takes tensor memory before it waits for
-  // this one must not get ahead of a block of this one that still needs its own.
+  // Only now: a dependent kernel takes its tensor memory before it waits for this
+  // one, and must not get ahead of a block of this one that still needs its own.
   griddep_launch_dependents();
 }
 
@@ -346,32 +361,29 @@ struct ShrinkArgs {
 };
 
 template <bool BF16, bool GMN>
-__global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUtensorMap tmT,
-                                                     const __grid_constant__ CUtensorMap tmT1,
-                                                     const __grid_constant__ CUtensorMap tmG, const ShrinkArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+__device__ __forceinline__ void shrink_body(uint8_t* smem, const CUtensorMap& tmT, const CUtensorMap& tmT1,
+                                            const CUtensorMap& tmG, const ShrinkArgs& a, int tile) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = cluster_nctarank(), rank = cluster_ctarank();
-  griddep_wait();
-  const int tile = blockIdx.x / cs;
-  if (tile >= a.plan.hdr[0]) return;
-  const int4 t = a.plan.tiles[tile];
-  const int adapter = t.x, pos = t.y, count = t.z;
   const int R = a.R, vecs = R / 8;
+  const int Rn = round16(R);
+  const int stage_bytes = kTile * 128 + a.gbytes;
+  const int ring_bytes = a.stages * stage_bytes, part_bytes = kTile * (R + 4) * 4;
+  const Ring ring = ring_at(smem + (ring_bytes > part_bytes ? ring_bytes : part_bytes));
+  ring_init(ring, tmem_cols(Rn), warp);
+  const uint32_t tmem = *ring.tmem;
+  griddep_wait();
+  const int4 t = tile < a.plan.hdr[0] ? a.plan.tiles[tile] : make_int4(-1, 0, 0, 0);
+  const int adapter = t.x, pos = t.y, count = t.z;
   uint16_t* P = static_cast<uint16_t*>(a.P);
-  if (adapter < 0) {  // rows without an adapter: zeros
+  if (adapter < 0) {  // rows without an adapter: zeros; past the last tile: nothing
+    if (warp == 1) tmem_dealloc(tmem, tmem_cols(Rn));
     if (rank == 0)
       for (int i = threadIdx.x; i < count * vecs; i += blockDim.x)
         *reinterpret_cast<uint4*>(P + int64_t(a.plan.perm[pos + i / vecs]) * a.ldp + (i % vecs) * 8) =
             make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  const int Rn = round16(R);
-  const int stage_bytes = kTile * 128 + a.gbytes;
-  const Ring ring = ring_at(smem + a.stages * stage_bytes);
-  ring_init(ring, tmem_cols(Rn), warp);
-  const uint32_t tmem = *ring.tmem;
   const int nkb = (a.D + 63) / 64;
   const int kb0 = int(int64_t(nkb) * rank / cs), n = int(int64_t(nkb) * (rank + 1) / cs) - kb0;
 
@@ -379,10 +391,9 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
     const TileRows rows = tile_rows(a.plan.perm, pos, count, lane, a.M);
     const uint32_t tx = rows_bytes<false>(rows, 4, 128) + a.gbytes;
     int i = 0;
-    for (; i < n; ++i) {
-      const int s = i % a.stages;
-      const uint32_t use = i / a.stages;
-      if (use > 0 && !mbar_wait_warp(&ring.empty[s], (use - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
+    for (Turn r(a.stages); i < n; ++i, r.next()) {
+      const int s = r.s;
+      if (!mbar_wait_warp(&ring.empty[s], r.ph ^ 1u, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
       uint8_t* st = smem + s * stage_bytes;
       const int k = (kb0 + i) * 64;
       if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], tx);
@@ -404,17 +415,17 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = instr_desc_major(BF16, kTile, Rn, 0, GMN ? 1 : 0);
-      for (int i = 0; i < n; ++i) {
-        const int s = i % a.stages;
-        if (!mbar_wait(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
+      const uint64_t ad0 = desc_k_major(smem);
+      const uint64_t bd0 = GMN ? desc_rows(smem + kTile * 128, a.rowb, 8192) : desc_k_major(smem + kTile * 128);
+      const int bstep = (GMN ? 16 * a.rowb : 32) >> 4;
+      Turn r(a.stages);
+      for (int i = 0; i < n; ++i, r.next()) {
+        if (!mbar_wait(&ring.full[r.s], r.ph, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
         tc_fence_after();
-        uint8_t* st = smem + s * stage_bytes;
-        const uint64_t ad = desc_k_major(st);
-        const uint64_t bd = GMN ? desc_rows(st + kTile * 128, a.rowb, 8192) : desc_k_major(st + kTile * 128);
-        const int bstep = (GMN ? 16 * a.rowb : 32) >> 4;
+        const uint64_t ad = ad0 + ((r.s * stage_bytes) >> 4), bd = bd0 + ((r.s * stage_bytes) >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) tc_mma(tmem, ad + ((32 * k) >> 4), bd + k * bstep, idesc, (i | k) != 0);
-        tc_commit(&ring.empty[s]);
+        tc_commit(&ring.empty[r.s]);
       }
       tc_commit(ring.done);
     }
@@ -467,294 +478,407 @@ __global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUt
   cluster_sync();  // no block leaves while another may still read its shared memory
 }
 
-// ---- expand: Y [rows][C] = base + s P [rows][R] . G^T ---------------------------------
-// A block of work is a tile and 128 columns; each SM's block takes an equal,
-// consecutive share of them all and keeps the loads of the next ones under
-// way (one block a tile and 128 columns, started anew each time, took 165 us
-// for [8192, 16384] where this one's traffic takes 82).
-//   warp 0    producer: base and G of the next blocks into the ring, P of the
-//             next tile into one of two slots
-//   warp 1    MMAs (one thread), tensor memory
-//   warps 2-9 two a quarter of the rows, 64 columns each: accumulator + base
-//             from the ring, rounded in place and stored from there (a box
-//             where the rows are consecutive, else coalesced stores)
-//   GMN false: G = B_l [C][R];  GMN true: G = A_l [R][C]
-struct ExpandArgs {
+template <bool BF16, bool GMN>
+__global__ void __launch_bounds__(128) shrink_kernel(const __grid_constant__ CUtensorMap tmT,
+                                                     const __grid_constant__ CUtensorMap tmT1,
+                                                     const __grid_constant__ CUtensorMap tmG, const ShrinkArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  shrink_body<BF16, GMN>(align1024(smem_raw), tmT, tmT1, tmG, a, blockIdx.x / cluster_nctarank());
+}
+
+// ---- expand in registers ------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight 16-bit columns from c of a row of C, those past its end 0 (or unwritten).
+__device__ __forceinline__ uint4 load_cols8(const uint16_t* row, int c, int C) {
+  if (c + 8 <= C) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (c + e < C) w[e >> 1] |= static_cast<uint32_t>(row[c + e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_cols8(uint16_t* row, int c, int C, const uint4& v) {
+  if (c + 8 <= C) {
+    *reinterpret_cast<uint4*>(row + c) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (c + e < C) row[c + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+constexpr int kRegCols = 64;  // columns of a warp
+// Warps of a block: `RG` (1 or 4) take the tile's groups of 32 rows between
+// them, 4 / 2 blocks of columns side by side.
+template <int RG>
+struct RegShape {
+  static constexpr int CG = RG == 1 ? 4 : 2;
+  static constexpr int THREADS = 32 * RG * CG;
+  static constexpr int COLS = CG * kRegCols;
+  static constexpr int PITCH = COLS * 2 + 16;  // bytes of a staged row of G
+};
+
+struct ExpandRegArgs {
   Plan plan;
   const float* scale;  // nullptr: 1
-  const void* base;    // nullptr: 0
-  void* Y;
-  int64_t ldb, ldy;
-  int M, C, R, stages, rowb, pbytes, gbytes;
+  const uint16_t* P;
+  const uint16_t* G;
+  const uint16_t* base;  // nullptr: 0
+  uint16_t* Y;
+  int64_t ldp, ldb, ldy;
+  int C, R;
+};
+
+// The k index of an MMA step may be dealt to lanes in any order that both
+// operands share, and so may its n index: lane t of a quad takes 4 consecutive
+// k of a step (8 of a pair of steps), one load a row, and n-tile j of 32
+// columns holds columns 8 t + 2 j and the next, so that a lane ends up with 8
+// consecutive columns of a row: one 16-byte load of base and one store.
+//   KS: steps of 16 with G in registers (1 or 2); 0: any number, read per 32 rows
+template <bool BF16, bool GMN, int KS, int RG>
+__global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 1 ? 4 : 2) expand_reg_kernel(const ExpandRegArgs a) {
+  using Sh = RegShape<RG>;
+  constexpr int kRegThreads = Sh::THREADS, kRegBlockCols = Sh::COLS, kRegPitch = Sh::PITCH;
+  extern __shared__ __align__(16) uint8_t gsm[];
+  const int warp = (threadIdx.x >> 5) % Sh::CG, lane = threadIdx.x & 31;
+  const int first = 32 * ((threadIdx.x >> 5) / Sh::CG);  // this warp's first rows of the tile
+  const int g = lane >> 2, q = lane & 3;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int4 t = a.plan.tiles[blockIdx.y];
+  if (int(blockIdx.y) >= a.plan.hdr[0]) return;
+  const int adapter = t.x, pos = t.y, count = t.z;
+  if (adapter < 0 && a.base == a.Y) return;
+  const int nb = blockIdx.x * kRegBlockCols;
+  const int n0 = nb + warp * kRegCols;
+  const int c0 = n0 + 8 * q;  // this lane's columns: c0 .. and c0 + 32 ..
+  // a group of 32 rows: g, g + 8, g + 16, g + 24 are this lane's
+  auto find = [&](int r0, int (&rows)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + 8 * k + g;
+      rows[k] = r < count ? a.plan.perm[pos + r] : -1;
+    }
+  };
+  auto fetch = [&](const int (&rows)[4], int h, uint4 (&x)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.base && rows[k] >= 0 && c0 + 32 * h < a.C)
+        x[k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c0 + 32 * h, a.C);
+    }
+  };
+  auto put = [&](const int (&rows)[4], int h, const uint4 (&x)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (rows[k] >= 0 && c0 + 32 * h < a.C)
+        store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c0 + 32 * h, a.C, x[k]);
+  };
+  int rows[4];
+  uint4 x[2][4];
+  find(first, rows);
+  fetch(rows, 0, x[0]);
+  fetch(rows, 1, x[1]);
+  if (adapter < 0) {
+    for (int r0 = first; r0 < count; r0 += 32 * RG) {
+      int next[4];
+      find(r0 + 32 * RG, next);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        put(rows, h, x[h]);
+        fetch(next, h, x[h]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rows[k] = next[k];
+    }
+    return;
+  }
+  const float scale = a.scale ? a.scale[adapter] : 1.f;
+  const uint16_t* G = a.G + int64_t(adapter) * a.C * a.R;
+  if constexpr (GMN) {
+    // G is [R][C]: its columns of this block to shared memory, rows and columns
+    // in the order that the fragments take them; zeros past R and C
+    const int krows = KS == 1 ? 16 : (a.R + 31) / 32 * 32;
+    for (int i = threadIdx.x; i < krows * (kRegBlockCols / 8); i += kRegThreads) {
+      const int k = i / (kRegBlockCols / 8), v = i % (kRegBlockCols / 8);
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (k < a.R && nb + 8 * v < a.C) w = *reinterpret_cast<const uint4*>(G + int64_t(k) * a.C + nb + 8 * v);
+      const int kp = KS == 1 ? 8 * ((k >> 1) & 1) + 2 * (k >> 2) + (k & 1)
+                             : (k & ~31) + 16 * ((k >> 2) & 1) + 8 * ((k >> 1) & 1) + 2 * ((k >> 3) & 3) + (k & 1);
+      uint32_t* to = reinterpret_cast<uint32_t*>(gsm + kp * kRegPitch + (v >> 2) * 64 + (v & 3) * 4);
+      to[0] = w.x;
+      to[4] = w.y;
+      to[8] = w.z;
+      to[12] = w.w;
+    }
+    __syncthreads();
+  }
+  if (n0 >= a.C || first >= count) return;
+  // fragments of G for step pair kb (KS == 1: the one step) and half h: b[j][step][2]
+  auto load_b = [&](int kb, int h, uint32_t (&b)[4][KS == 1 ? 1 : 2][2]) {
+    if constexpr (GMN) {
+#pragma unroll
+      for (int s = 0; s < (KS == 1 ? 1 : 2); ++s)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          // matrices: k rows 0-7 and 8-15 of tile j, then of tile j + 1
+          const uint32_t at = smem_addr(gsm + (kb * 32 + s * 16 + (lane & 15)) * kRegPitch +
+                                        (warp * kRegCols + 32 * h) * 2 + (j + (lane >> 4)) * 16);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(b[j][s][0]), "=r"(b[j][s][1]), "=r"(b[j + 1][s][0]), "=r"(b[j + 1][s][1])
+                       : "r"(at));
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int n = n0 + 32 * h + 8 * (g >> 1) + 2 * j + (g & 1);
+        n = n < a.C ? n : a.C - 1;  // a column past the end is not stored
+        const uint16_t* from = G + int64_t(n) * a.R;
+        if constexpr (KS == 1) {
+          const uint2 w = 4 * q < a.R ? *reinterpret_cast<const uint2*>(from + 4 * q) : make_uint2(0u, 0u);
+          b[j][0][0] = w.x;
+          b[j][0][1] = w.y;
+        } else {
+          const int k = kb * 32 + 8 * q;
+          const uint4 w = k < a.R ? *reinterpret_cast<const uint4*>(from + k) : make_uint4(0u, 0u, 0u, 0u);
+          b[j][0][0] = w.x;
+          b[j][0][1] = w.y;
+          b[j][1][0] = w.z;
+          b[j][1][1] = w.w;
+        }
+      }
+    }
+  };
+  auto load_a = [&](const int (&rows)[4], int kb, uint32_t (&f)[2][KS == 1 ? 1 : 2][4]) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = rows[2 * m + r];
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (KS == 1) {
+          if (row >= 0 && 4 * q < a.R) {
+            const uint2 u = *reinterpret_cast<const uint2*>(a.P + int64_t(row) * a.ldp + 4 * q);
+            w.x = u.x;
+            w.y = u.y;
+          }
+          f[m][0][r] = w.x;
+          f[m][0][2 + r] = w.y;
+        } else {
+          const int k = kb * 32 + 8 * q;
+          if (row >= 0 && k < a.R) w = *reinterpret_cast<const uint4*>(a.P + int64_t(row) * a.ldp + k);
+          f[m][0][r] = w.x;
+          f[m][0][2 + r] = w.y;
+          f[m][1][r] = w.z;
+          f[m][1][2 + r] = w.w;
+        }
+      }
+  };
+  constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
+  uint32_t held[KS ? 2 : 1][4][S][2];
+  if constexpr (KS > 0) {
+    load_b(0, 0, held[0]);
+    load_b(0, 1, held[1]);
+  }
+  // The next group's rows of P and base are read as soon as their registers
+  // are free, half by half: with all reads at the head of a group the kernel
+  // waited for them (16 warps an SM) and took 103 us for [8192, 16384].
+  uint32_t f[2][S][4];
+  if constexpr (KS > 0) load_a(rows, 0, f);
+  for (int r0 = first; r0 < count; r0 += 32 * RG) {
+    int next[4];
+    find(r0 + 32 * RG, next);
+    const int pairs = KS ? 1 : (a.R + 31) / 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float acc[2][4][4];  // [m tile][n tile]
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+      for (int kb = 0; kb < pairs; ++kb) {
+        if constexpr (KS == 0) {
+          load_a(rows, kb, f);
+          load_b(kb, h, held[0]);
+        }
+        const auto& b = held[KS ? h : 0];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16816<BF16>(acc[m][j], f[m][s], b[j][s][0], b[j][s][1]);
+      }
+      if constexpr (KS > 0) {
+        if (h == 1) load_a(next, 0, f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float(&d)[4][4] = acc[k >> 1];
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x[h][k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 b = unpack2<BF16>(w[j]);
+          w[j] = pack2<BF16>(fmaf(scale, d[j][2 * (k & 1)], b.x), fmaf(scale, d[j][2 * (k & 1) + 1], b.y));
+        }
+      }
+      put(rows, h, x[h]);
+      fetch(next, h, x[h]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rows[k] = next[k];
+  }
+}
+
+// ---- expand for larger R: the same with tcgen05 ------------------------------------------
+// One block a tile and 128 columns.  The product comes from one MMA chain over
+// R (with mma.sync the operands' traffic through L1 grows with R: 198 us for
+// [8192, 16384] at R = 64, 300 us at R = 128); base is read into registers
+// before it and added in the same layout, which tcgen05.ld 16x256b and a
+// permuted order of G's columns in shared memory give: a lane has 8
+// consecutive columns of a row.
+struct ExpandTcArgs {
+  ExpandRegArgs a;
   uint32_t* err;
 };
-
-constexpr int kExpCols = 128;
-constexpr int kExpThreads = 320;
-constexpr int kYBytes = kTile * kExpCols * 2;
-
-// The consecutive share of the blocks of work that this thread block takes,
-// one by one: column block nb of tile `tile`.
-struct Share {
-  int left, tile, nb, nblk;
-  bool fresh;  // the first block of its tile here
-  __device__ Share(int tiles, int nblk_) : nblk(nblk_), fresh(true) {
-    const int64_t total = int64_t(tiles) * nblk_;
-    const int64_t w = total * blockIdx.x / gridDim.x;
-    left = int(total * (blockIdx.x + 1) / gridDim.x - w);
-    tile = int(w / nblk_);
-    nb = int(w - int64_t(tile) * nblk_);
-  }
-  __device__ bool more() const { return left > 0; }
-  __device__ bool last_of_tile() const { return left == 1 || nb + 1 == nblk; }
-  __device__ void next() {
-    --left;
-    fresh = false;
-    if (++nb == nblk) {
-      nb = 0;
-      ++tile;
-      fresh = true;
-    }
-  }
-};
+constexpr int kTcCols = 128;
 
 template <bool BF16, bool GMN>
-__global__ void __launch_bounds__(kExpThreads, 1)
-    expand_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmG,
-                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB1,
-                  const __grid_constant__ CUtensorMap tmY, const ExpandArgs a) {
+__global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta) {
+  const ExpandRegArgs& a = ta.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = kYBytes + a.gbytes;
-  uint8_t* Ps = smem + a.stages * stage_bytes;  // two slots
-  const Ring ring = ring_at(Ps + 2 * a.pbytes);
-  uint64_t* acc_full = ring.more;       // two accumulators
-  uint64_t* acc_empty = ring.more + 2;
-  uint64_t* p_full = ring.more + 4;     // two slots of P
-  uint64_t* p_empty = ring.more + 6;
-  const int counts[8] = {1, 1, 8, 8, 1, 1, 1, 1};
-  griddep_wait();
-  ring_init(ring, 2 * kExpCols, warp, 8, counts);
+  const int g = lane >> 2, q = lane & 3;
+  const int R = a.R, Rn = round16(R), halves = R > 64 ? 2 : 1;
+  uint8_t* Ps = smem;                           // [128 rows][R], K-major
+  uint8_t* Gs = Ps + halves * kTile * 128;      // [128 columns][R], K-major, or [R][2 x 64 columns], N-major
+  const Ring ring = ring_at(Gs + (GMN ? 2 * Rn * 128 : halves * kTcCols * 128));
+  ring_init(ring, kTcCols, warp);
   const uint32_t tmem = *ring.tmem;
-  const int halves = a.R > 64 ? 2 : 1;
-  const int Rn = round16(a.R);
-  Share w(a.plan.hdr[0], (a.C + kExpCols - 1) / kExpCols);
-  const bool has_base = a.base != nullptr;
-  const bool in_place = a.base == a.Y;
-  // Every role walks the same blocks: i counts those that are not skipped
-  // (rows without an adapter whose base is already in place), p those tiles
-  // that need a slot of P.
-  if (warp == 0) {
-    int i = 0, p = 0;
-    int4 t = make_int4(-1, 0, 0, 0);
-    TileRows rows;
-    uint32_t bytes = 0;
-    for (; w.more(); w.next()) {
-      const int n0 = w.nb * kExpCols;
-      if (w.fresh) {
-        t = a.plan.tiles[w.tile];
-        rows = tile_rows(a.plan.perm, t.y, t.z, lane, a.M);
-        bytes = rows_bytes<false>(rows, 4, 128);
-      }
-      if (t.x < 0 && in_place) continue;
-      if (w.fresh && t.x >= 0) {
-        const int slot = p & 1;
-        if (p >= 2 && !mbar_wait_warp(&p_empty[slot], ((p >> 1) - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
-        const int fours = (t.z + 3) / 4;
-        if (lane == 0) mbar_arrive_expect_tx(&p_full[slot], halves * fours * 4 * a.rowb);
-        __syncwarp();
-        for (int h = 0; h < halves; ++h)
-          if (lane < fours)
-            tma_gather4(Ps + slot * a.pbytes + h * kTile * a.rowb + lane * 4 * a.rowb, &tmP, 64 * h, rows.rows,
-                        &p_full[slot]);
-        ++p;
-      }
-      const int s = i % a.stages;
-      const int use = i / a.stages;
-      if (use > 0 && !mbar_wait_warp(&ring.empty[s], (use - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
-      uint8_t* st = smem + s * stage_bytes;
-      const int subs = a.C - n0 > 64 ? 2 : 1;
-      if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], (has_base ? subs * bytes : 0u) + (t.x >= 0 ? a.gbytes : 0));
-      __syncwarp();
-      if (has_base)
-        for (int j = 0; j < subs; ++j)
-          rows_load<false>(rows, 4, 128, st + j * kTile * 128, &tmB, &tmB1, n0 + 64 * j, &ring.full[s], lane);
-      if (t.x >= 0 && lane == 0) {
-        uint8_t* g = st + kYBytes;
-        if constexpr (GMN) {
-          tma_load_3d(g, &tmG, n0, 0, t.x, &ring.full[s]);
-          tma_load_3d(g + Rn * 128, &tmG, n0 + 64, 0, t.x, &ring.full[s]);
-        } else {
-          for (int h = 0; h < halves; ++h)
-            tma_load_3d(g + h * kExpCols * a.rowb, &tmG, 64 * h, n0, t.x, &ring.full[s]);
-        }
-      }
-      __syncwarp();
-      ++i;
+  griddep_wait();
+  const int4 t = a.plan.tiles[blockIdx.y];
+  const int adapter = t.x, pos = t.y, count = t.z;
+  const bool none = adapter < 0;
+  if (int(blockIdx.y) >= a.plan.hdr[0] || (none && a.base == a.Y)) {
+    if (warp == 1) tmem_dealloc(tmem, kTcCols);
+    return;
+  }
+  const int n0 = blockIdx.x * kTcCols;
+  const int c0 = n0 + 8 * q;  // this lane's columns: c0 .. of each 32
+  int rows[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 32 * warp + 8 * k + g;
+    rows[k] = r < count ? a.plan.perm[pos + r] : -1;
+  }
+  uint4 x[4][4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[h][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.base && rows[k] >= 0 && c0 + 32 * h < a.C)
+        x[h][k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c0 + 32 * h, a.C);
     }
-    if (lane == 0) {  // nothing is in flight when the block ends
-      for (int q = i > a.stages ? i - a.stages : 0; q < i; ++q)
-        tail_wait(&ring.full[q % a.stages], (q / a.stages) & 1, a.err);
-      for (int q = p > 2 ? p - 2 : 0; q < p; ++q) tail_wait(&p_full[q & 1], (q >> 1) & 1, a.err);
+  if (!none) {
+    // operands in 128-byte swizzled rows of 64: piece c of row r sits at c ^ (r % 8).
+    // All copies are under way before any is waited for: with loads and stores
+    // through registers R = 64 took 182 us.
+    const int pieces = Rn / 8;
+    for (int i = threadIdx.x; i < count * pieces; i += 128) {
+      const int r = i / pieces, c = i - r * pieces;
+      const bool ok = 8 * c < R;
+      cp_async16(Ps + (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                 a.P + int64_t(a.plan.perm[pos + r]) * a.ldp + (ok ? 8 * c : 0), ok);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = instr_desc_major(BF16, kTile, kExpCols, 0, GMN ? 1 : 0);
-      int i = 0, p = 0, adapter = -1;
-      for (; w.more(); w.next()) {
-        if (w.fresh) adapter = a.plan.tiles[w.tile].x;
-        if (adapter < 0 && in_place) continue;
-        if (w.fresh && adapter >= 0) {
-          if (!mbar_wait(&p_full[p & 1], (p >> 1) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
-          ++p;
-        }
-        const int s = i % a.stages, b = i & 1;
-        if (!mbar_wait(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
-        if (i >= 2 && !mbar_wait(&acc_empty[b], ((i >> 1) - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC_FREE)) break;
-        tc_fence_after();
-        if (adapter >= 0) {
-          const uint8_t* P = Ps + ((p - 1) & 1) * a.pbytes;
-          const uint8_t* G = smem + s * stage_bytes + kYBytes;
-          const int ksub = a.rowb / 32;  // MMA steps in a row of an operand tile
-          for (int k = 0; k < Rn / 16; ++k) {
-            const int h = k / ksub, kk = k - h * ksub;
-            const uint64_t ad = desc_rows(P + h * kTile * a.rowb, a.rowb, 16) + ((32 * kk) >> 4);
-            const uint64_t bd = GMN ? desc_mn_major(G + 2048 * k, Rn * 128)
-                                    : desc_rows(G + h * kExpCols * a.rowb, a.rowb, 16) + ((32 * kk) >> 4);
-            tc_mma(tmem + b * kExpCols, ad, bd, idesc, k != 0);
-          }
-          if (w.last_of_tile()) tc_commit(&p_empty[(p - 1) & 1]);
-        }
-        tc_commit(&acc_full[b]);
-        ++i;
+    const uint16_t* G = a.G + int64_t(adapter) * a.C * R;
+    // column 32 i + 8 j + 2 k + e of the MMA is column 32 i + 8 k + 2 j + e of G
+    if constexpr (GMN) {
+      for (int i = threadIdx.x; i < Rn * (kTcCols / 2); i += 128) {  // pairs of columns
+        const int k = i / (kTcCols / 2), v = i % (kTcCols / 2);
+        const int c = 4 * ((v >> 4) & 1) + (v & 3);  // piece of the 64 columns, and 4 bytes of it
+        const bool ok = k < R && n0 + 2 * v < a.C;
+        cp_async4(Gs + (v >> 5) * Rn * 128 + k * 128 + ((c ^ (k & 7)) << 4) + ((v >> 2) & 3) * 4,
+                  G + (ok ? int64_t(k) * a.C + n0 + 2 * v : 0), ok);
+      }
+    } else {
+      for (int i = threadIdx.x; i < kTcCols * pieces; i += 128) {
+        const int v = i / pieces, c = i - v * pieces;  // column v of the block, piece c of its row
+        const int n = (v & ~31) + 8 * ((v >> 1) & 3) + 2 * ((v >> 3) & 3) + (v & 1);  // its place (the order is its own inverse)
+        const bool ok = n0 + v < a.C && 8 * c < R;
+        cp_async16(Gs + (c >> 3) * kTcCols * 128 + n * 128 + (((c & 7) ^ (n & 7)) << 4),
+                   G + (ok ? int64_t(n0 + v) * R + 8 * c : 0), ok);
+      }
+    }
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const uint32_t idesc = instr_desc_major(BF16, kTile, kTcCols, 0, GMN ? 1 : 0);
+      for (int k = 0; k < Rn / 16; ++k) {
+        const uint64_t ad = desc_k_major(Ps + (k >> 2) * kTile * 128) + ((32 * (k & 3)) >> 4);
+        const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, Rn * 128)
+                                : desc_k_major(Gs + (k >> 2) * kTcCols * 128) + ((32 * (k & 3)) >> 4);
+        tc_mma(tmem, ad, bd, idesc, k != 0);
       }
       tc_commit(ring.done);
     }
     __syncwarp();
-    tail_wait(ring.done, 0, a.err);
-  } else {
-    const int quad = warp & 3, sub = (warp - 2) >> 2;
-    uint16_t* Y = static_cast<uint16_t*>(a.Y);
-    int i = 0, pending = -1;
-    int4 t = make_int4(-1, 0, 0, 0);
-    int mine = 0;       // this lane's row
-    bool run = false;   // the warp's 32 rows are consecutive, and all there
-    int rows_here = 0;
-    float scale = 0.f;
-    for (; w.more(); w.next()) {
-      const int n0 = w.nb * kExpCols + 64 * sub;
-      if (w.fresh) {
-        t = a.plan.tiles[w.tile];
-        rows_here = t.z - 32 * quad;
-        mine = lane < rows_here ? a.plan.perm[t.y + 32 * quad + lane] : 0;
-        const int first = __shfl_sync(0xffffffffu, mine, 0);
-        run = rows_here >= 32 && __all_sync(0xffffffffu, mine == first + lane);
-        scale = t.x < 0 ? 0.f : a.scale ? a.scale[t.x] : 1.f;
-      }
-      if (t.x < 0 && in_place) continue;
-      const int s = i % a.stages, b = i & 1;
-      // the copied rows' own barrier, then the accumulator's
-      bool ok = mbar_wait_warp(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC);
-      ok = ok && mbar_wait_warp(&acc_full[b], (i >> 1) & 1, ring.abort_flag, a.err, ERR_WAIT_ACC);
-      if (!ok) break;
-      tc_fence_after();
-      const int cols = min(64, a.C - n0);
-      uint8_t* buf = smem + s * stage_bytes + sub * kTile * 128 + quad * 32 * 128;
-      bool boxed = false;
-      if (rows_here > 0 && cols > 0) {
-        uint8_t* row = buf + lane * 128;
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t h[32];
-          if (t.x >= 0) {
-            tmem_ld_32x32b_x32(tmem + (uint32_t(32 * quad) << 16) + b * kExpCols + 64 * sub + c, h);
-            tmem_ld_wait(h);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) h[e] = 0u;
-          }
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            // 16-byte piece v of the row's 64 columns, where the swizzle puts it
-            uint4* at = reinterpret_cast<uint4*>(row + (((c / 8 + v) ^ (lane & 7)) << 4));
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (has_base) x = *at;
-            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-            if (t.x >= 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2<BF16>(xw[e]);
-                xw[e] = pack2<BF16>(fmaf(scale, __uint_as_float(h[8 * v + 2 * e]), f.x),
-                                    fmaf(scale, __uint_as_float(h[8 * v + 2 * e + 1]), f.y));
-              }
-            }
-            *at = x;
-          }
-        }
-        boxed = run && cols == 64;
-        if (boxed) {
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[b]);
-      if (boxed) {
-        if (lane == 0) {
-          tma_store_2d_saddr(&tmY, smem_addr(buf), n0, mine);
-          bulk_commit();
-          // the stage of the store before this one, once that has left shared memory
-          if (pending >= 0) {
-            bulk_wait_read<1>();
-            mbar_arrive(&ring.empty[pending]);
-          }
-        }
-        pending = s;
-      } else {
-        if (rows_here > 0 && cols > 0) {
-          // eight lanes a row, four rows at a time
-          for (int r = 0; r < 32; r += 4) {
-            const int rr = r + (lane >> 3), c = (lane & 7) * 8;
-            const int64_t to = __shfl_sync(0xffffffffu, mine, rr);
-            if (rr < rows_here && c < cols) {
-              const uint4 x = *reinterpret_cast<const uint4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-              uint16_t* o = Y + to * a.ldy + n0 + c;
-              if (c + 8 <= cols) {
-                *reinterpret_cast<uint4*>(o) = x;
-              } else {
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 7; ++e)
-                  if (c + e < cols) o[e] = static_cast<uint16_t>(xw[e >> 1] >> (16 * (e & 1)));
-              }
-            }
-          }
-        }
-        // generic reads of the stage come before the copies that refill it
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (pending >= 0) {
-            bulk_wait_read<0>();
-            mbar_arrive(&ring.empty[pending]);
-          }
-          mbar_arrive(&ring.empty[s]);
-        }
-        pending = -1;
-      }
-      ++i;
-    }
-    if (lane == 0) bulk_wait_all<0>();
+    tail_wait(ring.done, 0, ta.err);
     __syncwarp();
+    tc_fence_after();
+  }
+  const float scale = none ? 0.f : a.scale ? a.scale[adapter] : 1.f;
+  if (32 * warp < count) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if (!none) {
+        uint32_t lo[16], hi[16];  // rows g, g + 8 and g + 16, g + 24
+        const uint32_t at = tmem + (uint32_t(32 * warp) << 16) + 32 * h;
+        tmem_ld_16x256b_x4(at, lo);
+        tmem_ld_16x256b_x4(at + (16u << 16), hi);
+        tmem_ld_wait(lo, hi);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t(&d)[16] = k < 2 ? lo : hi;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x[h][k]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 b = unpack2<BF16>(w[j]);
+            w[j] = pack2<BF16>(fmaf(scale, __uint_as_float(d[4 * j + 2 * (k & 1)]), b.x),
+                               fmaf(scale, __uint_as_float(d[4 * j + 2 * (k & 1) + 1]), b.y));
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (rows[k] >= 0 && c0 + 32 * h < a.C)
+          store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c0 + 32 * h, a.C, x[h][k]);
+    }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kExpCols);
+    tmem_dealloc(tmem, kTcCols);
   }
 }
 
@@ -774,22 +898,29 @@ struct WgradArgs {
 constexpr int kWgCols = 128;
 
 template <bool BF16, bool OT>
-__global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUtensorMap tmT,
-                                                    const __grid_constant__ CUtensorMap tmT1,
-                                                    const __grid_constant__ CUtensorMap tmP,
-                                                    const __grid_constant__ CUtensorMap tmP1, const WgradArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+__device__ __forceinline__ void wgrad_body(uint8_t* smem, const CUtensorMap& tmT, const CUtensorMap& tmT1,
+                                           const CUtensorMap& tmP, const CUtensorMap& tmP1, const WgradArgs& a,
+                                           int block, int adapter) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = cluster_nctarank(), rank = cluster_ctarank();
-  griddep_wait();
-  const int adapter = blockIdx.y;
-  const int c0 = int(blockIdx.x / cs) * kWgCols;
+  const int R = a.R, vecs = R / 8, Rn = round16(R), halves = R > 64 ? 2 : 1;
+  const int c0 = block * kWgCols;
   const int cols = min(kWgCols, a.C - c0);
-  const int R = a.R, vecs = R / 8;
+  const int subs = (cols + 63) / 64;  // tiles of 64 columns inside the matrix
+  const int tbytes = (kWgCols / 64) * 8192;
+  const int pbytes = 64 * a.rowb;
+  const int stage_bytes = tbytes + halves * pbytes;
+  const int part_bytes = kWgCols * (R + 4) * 4;
+  const int ring_bytes = a.stages * stage_bytes;
+  const Ring ring = ring_at(smem + (ring_bytes > part_bytes ? ring_bytes : part_bytes));
+  const uint32_t tcols = tmem_cols(Rn);
+  ring_init(ring, tcols, warp);
+  const uint32_t tmem = *ring.tmem;
+  griddep_wait();
   const int start = a.plan.start[adapter], rows = a.plan.start[adapter + 1] - start;
   uint16_t* dG = static_cast<uint16_t*>(a.dG) + int64_t(adapter) * a.C * R;
   if (rows == 0) {  // an adapter without rows: zeros
+    if (warp == 1) tmem_dealloc(tmem, tcols);
     if (rank == 0) {
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
       if constexpr (OT) {
@@ -802,29 +933,17 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
     }
     return;
   }
-  const int Rn = round16(R), halves = R > 64 ? 2 : 1;
-  const int subs = (cols + 63) / 64;  // tiles of 64 columns inside the matrix
-  const int tbytes = (kWgCols / 64) * 8192;
-  const int pbytes = 64 * a.rowb;
-  const int stage_bytes = tbytes + halves * pbytes;
-  const int part_bytes = kWgCols * (R + 4) * 4;
-  const int ring_bytes = a.stages * stage_bytes;
-  const Ring ring = ring_at(smem + (ring_bytes > part_bytes ? ring_bytes : part_bytes));
-  const uint32_t tcols = tmem_cols(Rn);
-  ring_init(ring, tcols, warp);
-  const uint32_t tmem = *ring.tmem;
   const int chunks = (rows + 63) / 64;
   const int q0 = int(int64_t(chunks) * rank / cs), n = int(int64_t(chunks) * (rank + 1) / cs) - q0;
 
   if (warp == 0) {
     const uint32_t tx = subs * 8192 + halves * pbytes;
     int i = 0;
-    for (; i < n; ++i) {
-      const int s = i % a.stages;
-      const uint32_t use = i / a.stages;
+    for (Turn w(a.stages); i < n; ++i, w.next()) {
+      const int s = w.s;
       const int at = (q0 + i) * 64;
       const TileRows r = tile_rows(a.plan.perm, start + at, min(64, rows - at), lane, a.M);
-      if (use > 0 && !mbar_wait_warp(&ring.empty[s], (use - 1) & 1, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
+      if (!mbar_wait_warp(&ring.empty[s], w.ph ^ 1u, ring.abort_flag, a.err, ERR_WAIT_EMPTY)) break;
       uint8_t* st = smem + s * stage_bytes;
       if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], tx);
       __syncwarp();
@@ -840,16 +959,16 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = instr_desc_major(BF16, 128, Rn, 1, 1);
-      for (int i = 0; i < n; ++i) {
-        const int s = i % a.stages;
-        if (!mbar_wait(&ring.full[s], (i / a.stages) & 1, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
+      const uint64_t ad0 = desc_mn_major(smem, 8192), bd0 = desc_rows(smem + tbytes, a.rowb, pbytes);
+      Turn r(a.stages);
+      for (int i = 0; i < n; ++i, r.next()) {
+        if (!mbar_wait(&ring.full[r.s], r.ph, ring.abort_flag, a.err, ERR_WAIT_FULL)) break;
         tc_fence_after();
-        uint8_t* st = smem + s * stage_bytes;
-        const uint64_t ad = desc_mn_major(st, 8192), bd = desc_rows(st + tbytes, a.rowb, pbytes);
+        const uint64_t ad = ad0 + ((r.s * stage_bytes) >> 4), bd = bd0 + ((r.s * stage_bytes) >> 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma(tmem, ad + ((2048 * k) >> 4), bd + ((16 * a.rowb * k) >> 4), idesc, (i | k) != 0);
-        tc_commit(&ring.empty[s]);
+          tc_mma(tmem, ad + ((2048 * k) >> 4), bd + a.rowb * k, idesc, (i | k) != 0);
+        tc_commit(&ring.empty[r.s]);
       }
       tc_commit(ring.done);
     }
@@ -915,6 +1034,44 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
   cluster_sync();
 }
 
+template <bool BF16, bool OT>
+__global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUtensorMap tmT,
+                                                    const __grid_constant__ CUtensorMap tmT1,
+                                                    const __grid_constant__ CUtensorMap tmP,
+                                                    const __grid_constant__ CUtensorMap tmP1, const WgradArgs a,
+                                                    int blocks) {
+  extern __shared__ uint8_t smem_raw[];
+  const int unit = blockIdx.x / cluster_nctarank();
+  wgrad_body<BF16, OT>(align1024(smem_raw), tmT, tmT1, tmP, tmP1, a, unit % blocks, unit / blocks);
+}
+
+// ---- both readers of dY: U (shrink) and dB (wgrad) in one launch -------------------------
+// The first clusters take the row tiles; all of them are resident at once
+// and move along the columns, each rank through its own share of them.  The
+// others take the blocks of columns in the order in which the ranks reach them,
+// so that whichever reads a part of dY second finds it in L2.
+template <bool BF16>
+__global__ void __launch_bounds__(128) dual_kernel(const __grid_constant__ CUtensorMap tmT,
+                                                   const __grid_constant__ CUtensorMap tmT1,
+                                                   const __grid_constant__ CUtensorMap tmG,
+                                                   const __grid_constant__ CUtensorMap tmP,
+                                                   const __grid_constant__ CUtensorMap tmP1, const ShrinkArgs sa,
+                                                   const WgradArgs wa, int tiles, int blocks, int adapters) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const int cs = cluster_nctarank();
+  const int unit = blockIdx.x / cs;
+  if (unit < tiles) {
+    shrink_body<BF16, true>(smem, tmT, tmT1, tmG, sa, unit);
+  } else {
+    const int u = unit - tiles, k = u / adapters;  // k-th block of columns in the ranks' order
+    const int per = (blocks + cs - 1) / cs;
+    const int block = (k % cs) * per + k / cs;
+    // per * cs may be past the last block: such units have nothing to do
+    if (block < blocks) wgrad_body<BF16, false>(smem, tmT, tmT1, tmP, tmP1, wa, block, u % adapters);
+  }
+}
+
 // ---- host ---------------------------------------------------------------------------
 template <class K>
 spg_status prepare(K kern, int smem) {
@@ -928,85 +1085,145 @@ bool rows_maps(CUtensorMap* box, CUtensorMap* one, const void* p, int64_t cols, 
          make_tmap_2d_swz(one, p, 2, uint64_t(cols), uint64_t(rows), uint64_t(ld) * 2, rowb / 2, 1, rowb);
 }
 
-constexpr int kRingBudget = 100 * 1024;  // shared memory of a ring where two blocks share an SM
+int ring_stages(int budget, int stage) {
+  const int n = budget / stage;
+  return n > kMaxStages ? kMaxStages : n < 2 ? 2 : n;
+}
+
+// Maps, arguments and launch shape of a shrink; `budget` bytes of ring.
+template <bool GMN>
+struct ShrinkPlan {
+  CUtensorMap tmT, tmT1, tmG;
+  ShrinkArgs a;
+  int64_t tiles;
+  int cs, smem;
+  bool ok;
+  ShrinkPlan(const void* T, int64_t ldt, const void* G, const float* scale, const Plan& plan, void* P, int64_t ldp,
+             int64_t M, int64_t D, int64_t R, int64_t L, int budget, uint32_t* err) {
+    const int Rn = round16(int(R)), rowb = row_bytes_of(int(R));
+    ok = rows_maps(&tmT, &tmT1, T, D, M, ldt, 128) &&
+         (GMN ? make_tmap_3d(&tmG, G, R, D, L, 64, rowb) : make_tmap_3d(&tmG, G, D, R, L, Rn, 128));
+    const int gbytes = GMN ? 64 * rowb * (R > 64 ? 2 : 1) : Rn * 128;
+    const int stage = kTile * 128 + gbytes;
+    const int stages = ring_stages(budget, stage);
+    // blocks of a cluster: as many as let every tile of full groups be resident
+    // at once with two blocks an SM, each with at least two steps of its own
+    // (shrink of [8192, 4096], rank 16, alone: 17 us with 4, 20 us with 2 or 8)
+    const int64_t nkb = (D + 63) / 64, busy = (M + kTile - 1) / kTile;
+    tiles = max_tiles(M, L);
+    cs = 1;
+    while (cs < 8 && busy * 2 * cs <= 2 * sm_count() && nkb >= 4 * cs) cs *= 2;
+    const int ring = stages * stage, part = kTile * (int(R) + 4) * 4;
+    smem = (ring > part ? ring : part) + kBarBytes + 1024;
+    a = ShrinkArgs{plan, scale, P, ldp, int(M), int(D), int(R), stages, gbytes, rowb, err};
+  }
+};
 
 template <bool BF16, bool GMN>
 spg_status shrink(const void* T, int64_t ldt, const void* G, const float* scale, const Plan& plan, void* P, int64_t ldp,
                   int64_t M, int64_t D, int64_t R, int64_t L, uint32_t* err, cudaStream_t st) {
-  const int Rn = round16(int(R)), rowb = row_bytes_of(int(R));
-  CUtensorMap tmT, tmT1, tmG;
-  if (!rows_maps(&tmT, &tmT1, T, D, M, ldt, 128)) return SPG_ERR_CUDA;
-  if (!(GMN ? make_tmap_3d(&tmG, G, R, D, L, 64, rowb) : make_tmap_3d(&tmG, G, D, R, L, Rn, 128))) return SPG_ERR_CUDA;
-  const int gbytes = GMN ? 64 * rowb * (R > 64 ? 2 : 1) : Rn * 128;
-  const int stage = kTile * 128 + gbytes;
-  int stages = kRingBudget / stage;
-  stages = stages > kMaxStages ? kMaxStages : stages;
-  // blocks of a cluster: as many as let every tile of full groups be resident
-  // at once (two blocks an SM), each with at least two steps of its own
-  const int64_t tiles = max_tiles(M, L), nkb = (D + 63) / 64;
-  const int64_t busy = (M + kTile - 1) / kTile;
-  int cs = 1;
-  while (cs < 8 && busy * 2 * cs <= 2 * sm_count() && nkb >= 4 * cs) cs *= 2;
-  const int ring = stages * stage, part = kTile * (int(R) + 4) * 4;
-  const int smem = (ring > part ? ring : part) + kBarBytes + 1024;
-  if (part > ring) return SPG_ERR_UNSUPPORTED_SHAPE;
+  const ShrinkPlan<GMN> s(T, ldt, G, scale, plan, P, ldp, M, D, R, L, 100 * 1024, err);
   auto kern = shrink_kernel<BF16, GMN>;
-  if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const ShrinkArgs a{plan, scale, P, ldp, int(M), int(D), int(R), stages, gbytes, rowb, err};
-  return launch_pdl_cluster(kern, dim3(unsigned(tiles * cs)), dim3(128), smem, cs, st, tmT, tmT1, tmG, a) ==
-                 cudaSuccess
+  if (!s.ok || prepare(kern, s.smem) != SPG_OK) return SPG_ERR_CUDA;
+  return launch_pdl_cluster(kern, dim3(unsigned(s.tiles * s.cs)), dim3(128), s.smem, s.cs, st, s.tmT, s.tmT1, s.tmG,
+                            s.a) == cudaSuccess
              ? launch_status()
              : SPG_ERR_CUDA;
 }
 
+// Y = base + s P G^T.  Up to R = 32 the product is a matter of registers.
+// Beyond that tcgen05 does it where there are whole tiles (at least 64 rows
+// for each adapter that rows can have); few rows stay with the register kernel.
 template <bool BF16, bool GMN>
 spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale, const Plan& plan, const void* base,
                   int64_t ldb, void* Y, int64_t ldy, int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err,
                   cudaStream_t st) {
-  const int Rn = round16(int(R)), halves = R > 64 ? 2 : 1, rowb = row_bytes_of(int(R));
-  CUtensorMap tmP, tmP32, tmG, tmB, tmB1, tmY, tmY1;
-  if (!rows_maps(&tmP32, &tmP, P, R, M, ldp, rowb) || !rows_maps(&tmY, &tmY1, Y, C, M, ldy, 128) ||
-      !rows_maps(&tmB, &tmB1, base ? base : Y, C, M, base ? ldb : ldy, 128))
-    return SPG_ERR_CUDA;
-  if (!(GMN ? make_tmap_3d(&tmG, G, C, R, L, Rn, 128) : make_tmap_3d(&tmG, G, R, C, L, kExpCols, rowb)))
-    return SPG_ERR_CUDA;
-  const int pbytes = halves * kTile * rowb;
-  const int gbytes = GMN ? 2 * Rn * 128 : halves * kExpCols * rowb;
-  const int fixed = 2 * pbytes + kBarBytes + 1024;
-  int stages = (232448 - fixed) / (kYBytes + gbytes);
-  stages = stages > kMaxStages ? kMaxStages : stages;
-  const int smem = stages * (kYBytes + gbytes) + fixed;
-  auto kern = expand_kernel<BF16, GMN>;
-  if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const ExpandArgs a{plan, scale, base, Y, ldb, ldy, int(M), int(C), int(R), stages, rowb, pbytes, gbytes, err};
-  const int64_t work = max_tiles(M, L) * ((C + kExpCols - 1) / kExpCols);
-  const int64_t blocks = work < sm_count() ? work : sm_count();
-  return launch_pdl(kern, dim3(unsigned(blocks)), dim3(kExpThreads), smem, st, tmP, tmG, tmB, tmB1, tmY, a) ==
-                 cudaSuccess
-             ? launch_status()
-             : SPG_ERR_CUDA;
+  const ExpandRegArgs a{plan, scale, static_cast<const uint16_t*>(P), static_cast<const uint16_t*>(G),
+                        static_cast<const uint16_t*>(base), static_cast<uint16_t*>(Y), ldp, ldb, ldy, int(C), int(R)};
+  const unsigned tiles = unsigned(max_tiles(M, L));
+  if (R > 32 && M >= 64 * L) {
+    const int halves = R > 64 ? 2 : 1, Rn = round16(int(R));
+    const int smem = halves * kTile * 128 + (GMN ? 2 * Rn * 128 : halves * kTcCols * 128) + kBarBytes + 1024;
+    auto kern = expand_tc_kernel<BF16, GMN>;
+    if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
+    const ExpandTcArgs ta{a, err};
+    return launch_pdl(kern, dim3(unsigned((C + kTcCols - 1) / kTcCols), tiles), dim3(128), smem, st, ta) == cudaSuccess
+               ? launch_status()
+               : SPG_ERR_CUDA;
+  }
+  // Few whole tiles: their groups of 32 rows go to warps side by side (M 1024,
+  // C 4096: 16.0 against 17.4 us with a group after the other); otherwise a warp
+  // takes them in turn and keeps G ([8192, 16384]: 103 against 112 us; 16 rows of
+  // 8 adapters: 10.5 against 14.8).
+  const int64_t busy = M / kTile * ((C + 255) / 256);
+  auto go = [&](auto shape) -> spg_status {
+    constexpr int RG = decltype(shape)::value;
+    using Sh = RegShape<RG>;
+    auto kern = R <= 16   ? expand_reg_kernel<BF16, GMN, 1, RG>
+                : R <= 32 ? expand_reg_kernel<BF16, GMN, 2, RG>
+                          : expand_reg_kernel<BF16, GMN, 0, RG>;
+    const int smem = GMN ? (R <= 16 ? 16 : (int(R) + 31) / 32 * 32) * Sh::PITCH : 0;
+    if (smem > 48 * 1024 && prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
+    return launch_pdl(kern, dim3(unsigned((C + Sh::COLS - 1) / Sh::COLS), tiles), dim3(Sh::THREADS), smem, st, a) ==
+                   cudaSuccess
+               ? launch_status()
+               : SPG_ERR_CUDA;
+  };
+  return M >= 64 * L && busy > 0 && busy < 2 * sm_count() ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 1>());
 }
+
+// The same for a wgrad.
+struct WgradPlan {
+  CUtensorMap tmT, tmT1, tmP, tmP1;
+  WgradArgs a;
+  int64_t blocks;
+  int cs, smem;
+  bool ok;
+  WgradPlan(const void* T, int64_t ldt, const void* P, int64_t ldp, const float* scale, const Plan& plan, void* dG,
+            int64_t M, int64_t C, int64_t R, int64_t L, int budget, uint32_t* err) {
+    const int rowb = row_bytes_of(int(R));
+    ok = rows_maps(&tmT, &tmT1, T, C, M, ldt, 128) && rows_maps(&tmP, &tmP1, P, R, M, ldp, rowb);
+    const int stage = (kWgCols / 64) * 8192 + (R > 64 ? 2 : 1) * 64 * rowb;
+    const int stages = ring_stages(budget, stage);
+    blocks = (C + kWgCols - 1) / kWgCols;
+    // blocks of a cluster: some three rounds of four blocks an SM, with at
+    // least four steps each where the rows are spread over a few adapters
+    const int64_t groups = L < 4 ? L : 4;
+    cs = 1;
+    while (cs < 8 && blocks * groups * cs < 3 * sm_count() && M / groups >= 256 * cs) cs *= 2;
+    const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
+    smem = (ring > part ? ring : part) + kBarBytes + 1024;
+    a = WgradArgs{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
+  }
+};
 
 template <bool BF16, bool OT>
 spg_status wgrad(const void* T, int64_t ldt, const void* P, int64_t ldp, const float* scale, const Plan& plan, void* dG,
                  int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err, cudaStream_t st) {
-  const int rowb = row_bytes_of(int(R));
-  CUtensorMap tmT, tmT1, tmP, tmP1;
-  if (!rows_maps(&tmT, &tmT1, T, C, M, ldt, 128) || !rows_maps(&tmP, &tmP1, P, R, M, ldp, rowb)) return SPG_ERR_CUDA;
-  const int stage = (kWgCols / 64) * 8192 + (R > 64 ? 2 : 1) * 64 * rowb;
-  int stages = kRingBudget / stage;
-  stages = stages > kMaxStages ? kMaxStages : stages;
-  const int64_t blocks = (C + kWgCols - 1) / kWgCols;
-  const int64_t groups = L < 4 ? L : 4;
-  int cs = 1;
-  while (cs < 8 && blocks * groups * cs < 4 * sm_count() && M / groups >= 256 * cs) cs *= 2;
-  const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
-  const int smem = (ring > part ? ring : part) + kBarBytes + 1024;
+  // a quarter of an SM's shared memory each: a block's first loads and last sums hide behind three others
+  // ([8192, 16384], rank 16, 8 adapters: 60 us; with two blocks an SM 95 us)
+  const WgradPlan w(T, ldt, P, ldp, scale, plan, dG, M, C, R, L, 50 * 1024, err);
   auto kern = wgrad_kernel<BF16, OT>;
-  if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-  const WgradArgs a{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
-  return launch_pdl_cluster(kern, dim3(unsigned(blocks * cs), unsigned(L)), dim3(128), smem, cs, st, tmT, tmT1, tmP,
-                            tmP1, a) == cudaSuccess
+  if (!w.ok || prepare(kern, w.smem) != SPG_OK) return SPG_ERR_CUDA;
+  return launch_pdl_cluster(kern, dim3(unsigned(w.blocks * L * w.cs)), dim3(128), w.smem, w.cs, st, w.tmT, w.tmT1,
+                            w.tmP, w.tmP1, w.a, int(w.blocks)) == cudaSuccess
+             ? launch_status()
+             : SPG_ERR_CUDA;
+}
+
+// U = s dY B_l and dB = s dY^T V from one reading of dY.
+template <bool BF16>
+spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale, const Plan& plan, void* U,
+                const void* V, int64_t ldv, void* dB, int64_t M, int64_t N, int64_t R, int64_t L, uint32_t* err,
+                cudaStream_t st) {
+  const ShrinkPlan<true> s(dY, lddy, B, scale, plan, U, R, M, N, R, L, 50 * 1024, err);
+  const WgradPlan w(dY, lddy, V, ldv, scale, plan, dB, M, N, R, L, 50 * 1024, err);
+  auto kern = dual_kernel<BF16>;
+  const int smem = s.smem > w.smem ? s.smem : w.smem;
+  if (!s.ok || !w.ok || prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
+  const int64_t units = (w.blocks + s.cs - 1) / s.cs * s.cs * L;
+  return launch_pdl_cluster(kern, dim3(unsigned((s.tiles + units) * s.cs)), dim3(128), smem, s.cs, st, s.tmT, s.tmT1,
+                            s.tmG, w.tmP, w.tmP1, s.a, w.a, int(s.tiles), int(w.blocks), int(L)) == cudaSuccess
              ? launch_status()
              : SPG_ERR_CUDA;
 }
@@ -1042,8 +1259,7 @@ spg_status backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
                     const void* B, const float* scale, const Plan& plan, const void* dbase, int64_t lddb, void* dX,
                     int64_t lddx, void* dA, void* dB, void* U, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
                     uint32_t* err, cudaStream_t st) {
-  spg_status rc = shrink<BF16, true>(dY, lddy, B, scale, plan, U, R, M, N, R, L, err, st);
-  if (rc == SPG_OK) rc = wgrad<BF16, false>(dY, lddy, V, ldv, scale, plan, dB, M, N, R, L, err, st);
+  spg_status rc = dual<BF16>(dY, lddy, B, scale, plan, U, V, ldv, dB, M, N, R, L, err, st);
   if (rc == SPG_OK) rc = wgrad<BF16, true>(X, ldx, U, R, nullptr, plan, dA, M, K, R, L, err, st);
   if (rc == SPG_OK && dX)
     rc = expand<BF16, true>(U, R, A, nullptr, plan, dbase, lddb, dX, lddx, M, K, R, L, err, st);
