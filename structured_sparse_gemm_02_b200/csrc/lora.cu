@@ -75,20 +75,27 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
   if (threadIdx.x == 0) carry = make_int2(0, 0);
   __syncthreads();
   const int strip = (M + warps * 32 - 1) / (warps * 32) * 32;
-  const int r0 = warp * strip, r1 = min(M, r0 + strip);
-  if (warp < warps) {
-    for (int r = r0; r < r1; r += 32) {
-      const int row = r + lane;
-      int a = -1;
-      if (row < r1) {
-        a = index[row];
-        if (a < 0 || a >= L) a = L;
-      }
-      const unsigned same = __match_any_sync(0xffffffffu, a);
-      if (a >= 0 && lane == __ffs(same) - 1) cnt[warp * G + a] += __popc(same);
-      __syncwarp();
-    }
-  }
+  const int r0 = warp * strip, r1 = warp < warps ? min(M, r0 + strip) : r0;
+  // the group of a row, -1 past the strip; the first kHeld steps of a strip are
+  // read once, all at the same time
+  constexpr int kHeld = 8;
+  auto group_at = [&](int row) {
+    if (row >= r1) return -1;
+    const int a = index[row];
+    return a < 0 || a >= L ? L : a;
+  };
+  int held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = group_at(r0 + 32 * k + lane);
+  auto count = [&](int a) {
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    if (a >= 0 && lane == __ffs(same) - 1) cnt[warp * G + a] += __popc(same);
+    __syncwarp();
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (r0 + 32 * k < r1) count(held[k]);
+  for (int r = r0 + 32 * kHeld; r < r1; r += 32) count(group_at(r + lane));
   __syncthreads();
   // rows and tiles before each group: a block scan over 1024 groups at a time
   for (int g0 = 0; g0 < G; g0 += blockDim.x) {
@@ -134,25 +141,21 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ 
     if (threadIdx.x == blockDim.x - 1) carry = make_int2(v.x + own.x, v.y + own.y);
     __syncthreads();
   }
-  if (warp < warps) {
-    for (int r = r0; r < r1; r += 32) {
-      const int row = r + lane;
-      int a = -1;
-      if (row < r1) {
-        a = index[row];
-        if (a < 0 || a >= L) a = L;
-      }
-      const unsigned same = __match_any_sync(0xffffffffu, a);
-      int at = 0;
-      if (a >= 0) at = cnt[warp * G + a];
-      __syncwarp();
-      if (a >= 0) {
-        p.perm[at + __popc(same & ((1u << lane) - 1))] = row;
-        if (lane == __ffs(same) - 1) cnt[warp * G + a] = at + __popc(same);
-      }
-      __syncwarp();
+  auto place = [&](int row, int a) {
+    const unsigned same = __match_any_sync(0xffffffffu, a);
+    int at = 0;
+    if (a >= 0) at = cnt[warp * G + a];
+    __syncwarp();
+    if (a >= 0) {
+      p.perm[at + __popc(same & ((1u << lane) - 1))] = row;
+      if (lane == __ffs(same) - 1) cnt[warp * G + a] = at + __popc(same);
     }
-  }
+    __syncwarp();
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (r0 + 32 * k < r1) place(r0 + 32 * k + lane, held[k]);
+  for (int r = r0 + 32 * kHeld; r < r1; r += 32) place(r + lane, group_at(r + lane));
 }
 
 // ---- shared pieces ------------------------------------------------------------------
@@ -883,8 +886,9 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
 }
 
 // ---- wgrad: dG_l [C][R] = s_l sum over l's rows of T[m][c] P[m][r] ----------------------
-// One cluster a block of kWgCols columns of T and an adapter; its blocks split
-// the adapter's rows in chunks of 64 and add their sums as shrink_kernel does.
+// A unit of work is a block of kWgCols columns of T and an adapter.  One block
+// takes it, or (parts > 1) all blocks of a cluster split the adapter's rows in
+// chunks of 64 and add their sums as shrink_kernel does.
 // Both operands are read with the row as the MMA's K index.
 //   OT false: dG is [C][R] (dB);  OT true: [R][C] (dA)
 struct WgradArgs {
@@ -900,9 +904,8 @@ constexpr int kWgCols = 128;
 template <bool BF16, bool OT>
 __device__ __forceinline__ void wgrad_body(uint8_t* smem, const CUtensorMap& tmT, const CUtensorMap& tmT1,
                                            const CUtensorMap& tmP, const CUtensorMap& tmP1, const WgradArgs& a,
-                                           int block, int adapter) {
+                                           int block, int adapter, int cs, int rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = cluster_nctarank(), rank = cluster_ctarank();
   const int R = a.R, vecs = R / 8, Rn = round16(R), halves = R > 64 ? 2 : 1;
   const int c0 = block * kWgCols;
   const int cols = min(kWgCols, a.C - c0);
@@ -992,7 +995,7 @@ __device__ __forceinline__ void wgrad_body(uint8_t* smem, const CUtensorMap& tmT
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();
+  cs > 1 ? cluster_sync() : __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, tcols);
@@ -1013,7 +1016,8 @@ __device__ __forceinline__ void wgrad_body(uint8_t* smem, const CUtensorMap& tmT
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int q = 0; q < cs; ++q) {
       if (int(int64_t(chunks) * (q + 1) / cs) == int(int64_t(chunks) * q / cs)) continue;  // a block without rows
-      const uint32_t from = mapa_shared(smem_addr(part + c * pitch + r), q);
+      const uint32_t at = smem_addr(part + c * pitch + r);
+      const uint32_t from = cs > 1 ? mapa_shared(at, q) : mapa_shared(at, cluster_ctarank());
       if constexpr (OT) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += ld_cluster_f(from + e * pitch * 4);
@@ -1031,7 +1035,7 @@ __device__ __forceinline__ void wgrad_body(uint8_t* smem, const CUtensorMap& tmT
     *reinterpret_cast<uint4*>(OT ? dG + int64_t(r) * a.C + c0 + c : dG + int64_t(c0 + c) * R + r) = o;
   }
   __syncwarp();
-  cluster_sync();
+  if (cs > 1) cluster_sync();
 }
 
 template <bool BF16, bool OT>
@@ -1042,21 +1046,26 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
                                                     int blocks) {
   extern __shared__ uint8_t smem_raw[];
   const int unit = blockIdx.x / cluster_nctarank();
-  wgrad_body<BF16, OT>(align1024(smem_raw), tmT, tmT1, tmP, tmP1, a, unit % blocks, unit / blocks);
+  wgrad_body<BF16, OT>(align1024(smem_raw), tmT, tmT1, tmP, tmP1, a, unit % blocks, unit / blocks, cluster_nctarank(),
+                       cluster_ctarank());
 }
 
 // ---- both readers of dY: U (shrink) and dB (wgrad) in one launch -------------------------
 // The first clusters take the row tiles; all of them are resident at once
 // and move along the columns, each rank through its own share of them.  The
 // others take the blocks of columns in the order in which the ranks reach them,
-// so that whichever reads a part of dY second finds it in L2.
+// so that whichever reads a part of dY second finds it in L2.  Where there are
+// units enough (parts == 1) each block of a cluster has one of its own: split
+// over the cluster, [2048, 16384] with 4 adapters took 74 us of 4096 blocks with
+// one chunk of rows each.
 template <bool BF16>
 __global__ void __launch_bounds__(128) dual_kernel(const __grid_constant__ CUtensorMap tmT,
                                                    const __grid_constant__ CUtensorMap tmT1,
                                                    const __grid_constant__ CUtensorMap tmG,
                                                    const __grid_constant__ CUtensorMap tmP,
                                                    const __grid_constant__ CUtensorMap tmP1, const ShrinkArgs sa,
-                                                   const WgradArgs wa, int tiles, int blocks, int adapters) {
+                                                   const WgradArgs wa, int tiles, int blocks, int adapters,
+                                                   int parts) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const int cs = cluster_nctarank();
@@ -1064,11 +1073,14 @@ __global__ void __launch_bounds__(128) dual_kernel(const __grid_constant__ CUten
   if (unit < tiles) {
     shrink_body<BF16, true>(smem, tmT, tmT1, tmG, sa, unit);
   } else {
-    const int u = unit - tiles, k = u / adapters;  // k-th block of columns in the ranks' order
+    const int rank = cluster_ctarank();
+    const int u = parts > 1 ? unit - tiles : (unit - tiles) * cs + rank;
+    const int k = u / adapters;  // k-th block of columns in the ranks' order
     const int per = (blocks + cs - 1) / cs;
     const int block = (k % cs) * per + k / cs;
-    // per * cs may be past the last block: such units have nothing to do
-    if (block < blocks) wgrad_body<BF16, false>(smem, tmT, tmT1, tmP, tmP1, wa, block, u % adapters);
+    // some places of the order are past the last block: nothing to do
+    if (k < per * cs && block < blocks)
+      wgrad_body<BF16, false>(smem, tmT, tmT1, tmP, tmP1, wa, block, u % adapters, parts, parts > 1 ? rank : 0);
   }
 }
 
@@ -1172,6 +1184,9 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
   return M >= 64 * L && busy > 0 && busy < 2 * sm_count() ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 1>());
 }
 
+// Adapters that can have whole tiles of rows.
+int64_t row_groups(int64_t M, int64_t L) { return L < M / kTile + 1 ? L : M / kTile + 1; }
+
 // The same for a wgrad.
 struct WgradPlan {
   CUtensorMap tmT, tmT1, tmP, tmP1;
@@ -1186,11 +1201,11 @@ struct WgradPlan {
     const int stage = (kWgCols / 64) * 8192 + (R > 64 ? 2 : 1) * 64 * rowb;
     const int stages = ring_stages(budget, stage);
     blocks = (C + kWgCols - 1) / kWgCols;
-    // blocks of a cluster: some three rounds of four blocks an SM, with at
-    // least four steps each where the rows are spread over a few adapters
-    const int64_t groups = L < 4 ? L : 4;
+    // blocks of a cluster: up to some three an SM, with at least four chunks
+    // each where the rows are spread evenly
+    const int64_t groups = row_groups(M, L);
     cs = 1;
-    while (cs < 8 && blocks * groups * cs < 3 * sm_count() && M / groups >= 256 * cs) cs *= 2;
+    while (cs < 8 && blocks * groups * cs < 2 * sm_count() && M / groups >= 256 * cs) cs *= 2;
     const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
     smem = (ring > part ? ring : part) + kBarBytes + 1024;
     a = WgradArgs{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
@@ -1222,8 +1237,13 @@ spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale,
   const int smem = s.smem > w.smem ? s.smem : w.smem;
   if (!s.ok || !w.ok || prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
   const int64_t units = (w.blocks + s.cs - 1) / s.cs * s.cs * L;
-  return launch_pdl_cluster(kern, dim3(unsigned((s.tiles + units) * s.cs)), dim3(128), smem, s.cs, st, s.tmT, s.tmT1,
-                            s.tmG, w.tmP, w.tmP1, s.a, w.a, int(s.tiles), int(w.blocks), int(L)) == cudaSuccess
+  // split a unit's rows over the cluster only where the units do not fill the
+  // device and each part keeps four chunks
+  const int64_t groups = row_groups(M, L);
+  const int parts = w.blocks * groups < sm_count() && M / groups >= 256 * s.cs ? s.cs : 1;
+  const int64_t clusters = s.tiles + (parts > 1 ? units : (units + s.cs - 1) / s.cs);
+  return launch_pdl_cluster(kern, dim3(unsigned(clusters * s.cs)), dim3(128), smem, s.cs, st, s.tmT, s.tmT1, s.tmG,
+                            w.tmP, w.tmP1, s.a, w.a, int(s.tiles), int(w.blocks), int(L), parts) == cudaSuccess
              ? launch_status()
              : SPG_ERR_CUDA;
 }
