@@ -110,15 +110,33 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_torch = None
+_FLOAT_CODES: dict = {}
+
+
+def _tm():
+    """torch, imported with the first call that needs it (the package itself also builds without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _FLOAT_CODES.update({torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32})
+        _torch = torch
+    return _torch
+
+
 def _check(fn: str, st: int) -> None:
     if st != 0:
         raise SpgError(fn, st)
 
 
 def _stream(stream) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(getattr(s, "cuda_stream", s))
+    if stream is None:
+        torch = _tm()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object (3 us) where torch offers that
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 def _dtype_code(t) -> int:
@@ -490,20 +508,6 @@ def spgemm_tw_f16_noalloc(X, desc: TwDesc, Y=None, stream=None):
     return Y
 
 
-_torch = None
-_FLOAT_CODES: dict = {}
-
-
-def _tm():
-    """torch, imported with the first call that needs it (the package itself also builds without it)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _FLOAT_CODES.update({torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32})
-        _torch = torch
-    return _torch
-
-
 def _like(t, name: str, dtype, shape, dev: int) -> int:
     """_arg for the further tensors of a call whose first one passed it (its device is
     ``dev``): a valid tensor costs a few comparisons, any other one gets _arg's message.
@@ -523,9 +527,11 @@ def _like(t, name: str, dtype, shape, dev: int) -> int:
 
 def _first(t, name: str, dtypes, dims: int = 2) -> int:
     """_arg for a call's first tensor; returns its row pitch."""
-    _arg(t, name, dtypes)
+    if not isinstance(t, _tm().Tensor) or t.dtype not in dtypes:
+        _arg(t, name, dtypes)
     if t.dim() != dims:
         raise ValueError(f"{name} must be {dims}-D")
+    _on_device(t, name)
     return _like(t, name, t.dtype, t.shape, t.get_device())
 
 
@@ -544,6 +550,9 @@ def _new(shape, dtype, like, stream, pad=False):
     if stream is not None and like.is_cuda:
         with _torch.cuda.stream(_on_stream(stream, like.device)):
             return _new(shape, dtype, like, None, pad)
+    if shape == like.shape and dtype is like.dtype and like.is_contiguous() and not (
+            pad and (shape[1] * dtype.itemsize) % 16):
+        return _torch.empty_like(like)  # the cheapest way to say the same
     if pad:
         M, C = shape
         step = 16 // dtype.itemsize
@@ -601,7 +610,8 @@ def _ln_fwd(fn, X, gamma, beta, eps, qscale, residual, H, Y, ydt, stats, stream)
     if qscale is None:
         mean = rstd = None
         if stats:
-            mean, rstd = _new((2, M), _torch.float32, X, stream).unbind()
+            mean = _new((M,), _torch.float32, X, stream)
+            rstd = _new((M,), _torch.float32, mean, stream)
         _check(fn, lib().layernorm(
             X.data_ptr(), ldx, res, ldres, h, ldh, gamma.data_ptr(), _ptr(beta), eps, Y.data_ptr(), ldy, _ptr(mean),
             _ptr(rstd), M, C, code, wcode, _stream(stream)))
@@ -640,10 +650,8 @@ def layernorm_bwd(dY, X, mean, rstd, gamma, dH=None, dX=None, dgamma=None, dbeta
     if dX is None:
         dX = _new(shape, dt, X, stream, pad=True)
     lddx = _like(dX, "dX", dt, shape, dev)
-    if dgamma is None and dbeta is None:
-        dgamma, dbeta = _new((2, C), wdt, X, stream).unbind()
-    dgamma = _new((C,), wdt, X, stream) if dgamma is None else dgamma
-    dbeta = _new((C,), wdt, X, stream) if dbeta is None else dbeta
+    dgamma = _new((C,), wdt, gamma, stream) if dgamma is None else dgamma
+    dbeta = _new((C,), wdt, gamma, stream) if dbeta is None else dbeta
     need = lib().layernorm_bwd_workspace_size(M, C, code)
     if workspace is None:
         workspace = _new((need,), _torch.uint8, X, stream)

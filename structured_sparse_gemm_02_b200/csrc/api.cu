@@ -104,6 +104,26 @@ bool make_tmap_2d_swz(CUtensorMap* map, const void* base, int esize, uint64_t co
   return r == CUDA_SUCCESS;
 }
 
+cudaError_t allow_smem(const void* kern, int smem) {
+  struct Entry { const void* k; int dev; int smem; };
+  static std::mutex mu;
+  static Entry cache[256];
+  static int used = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  Entry* at = nullptr;
+  for (int i = 0; i < used && !at; ++i)
+    if (cache[i].k == kern && cache[i].dev == dev) at = &cache[i];
+  if (at && at->smem >= smem) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  if (at) at->smem = smem;
+  else if (used < 256) cache[used++] = Entry{kern, dev, smem};
+  return cudaSuccess;
+}
+
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,
                   int swizzle_bytes) {
   std::call_once(g_encode_once, load_encode);

@@ -14,6 +14,10 @@ namespace spg {
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,
                   int swizzle_bytes);
 
+// Allows `kern` on the current device `smem` bytes of dynamic shared memory (a
+// runtime call only where it was allowed fewer before).
+cudaError_t allow_smem(const void* kern, int smem);
+
 // Four rows of a 2-D tensor (map box: one row) to four consecutive rows of
 // shared memory.  A row index past the tensor reads as zeros.
 __device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* m, int32_t x, int4 rows,

@@ -1087,8 +1087,7 @@ __global__ void __launch_bounds__(128) dual_kernel(const __grid_constant__ CUten
 // ---- host ---------------------------------------------------------------------------
 template <class K>
 spg_status prepare(K kern, int smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? SPG_OK
-                                                                                                      : SPG_ERR_CUDA;
+  return allow_smem(reinterpret_cast<const void*>(kern), smem) == cudaSuccess ? SPG_OK : SPG_ERR_CUDA;
 }
 
 // Rows of a matrix: boxes of 32 rows, and single rows for gathers, of `rowb` bytes.
@@ -1201,11 +1200,11 @@ struct WgradPlan {
     const int stage = (kWgCols / 64) * 8192 + (R > 64 ? 2 : 1) * 64 * rowb;
     const int stages = ring_stages(budget, stage);
     blocks = (C + kWgCols - 1) / kWgCols;
-    // blocks of a cluster: up to some three an SM, with at least four chunks
-    // each where the rows are spread evenly
+    // blocks of a cluster: up to some three an SM, with a chunk each where the
+    // rows are spread evenly
     const int64_t groups = row_groups(M, L);
     cs = 1;
-    while (cs < 8 && blocks * groups * cs < 2 * sm_count() && M / groups >= 256 * cs) cs *= 2;
+    while (cs < 8 && blocks * groups * cs < 2 * sm_count() && M / groups >= 64 * cs) cs *= 2;
     const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
     smem = (ring > part ? ring : part) + kBarBytes + 1024;
     a = WgradArgs{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
@@ -1237,10 +1236,8 @@ spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale,
   const int smem = s.smem > w.smem ? s.smem : w.smem;
   if (!s.ok || !w.ok || prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
   const int64_t units = (w.blocks + s.cs - 1) / s.cs * s.cs * L;
-  // split a unit's rows over the cluster only where the units do not fill the
-  // device and each part keeps four chunks
-  const int64_t groups = row_groups(M, L);
-  const int parts = w.blocks * groups < sm_count() && M / groups >= 256 * s.cs ? s.cs : 1;
+  // a unit's rows are split over the cluster only where the units do not fill the device
+  const int parts = w.blocks * row_groups(M, L) < sm_count() ? s.cs : 1;
   const int64_t clusters = s.tiles + (parts > 1 ? units : (units + s.cs - 1) / s.cs);
   return launch_pdl_cluster(kern, dim3(unsigned(clusters * s.cs)), dim3(128), smem, s.cs, st, s.tmT, s.tmT1, s.tmG,
                             w.tmP, w.tmP1, s.a, w.a, int(s.tiles), int(w.blocks), int(L), parts) == cudaSuccess

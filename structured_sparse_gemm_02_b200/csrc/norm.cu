@@ -941,7 +941,7 @@ cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int blocks, cudaStream_
     }
   }
   if (smem > 40 * 1024) {  // 48 KB with the static arrays
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(k, dim3(blocks), dim3(s.threads), smem, st, b);
