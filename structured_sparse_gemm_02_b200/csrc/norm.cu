@@ -110,72 +110,115 @@ struct Vec {
   }
 };
 
-// VE elements at p, of which the first n are inside the row.  WHOLE: all of
-// them are, and p is 16-byte aligned; otherwise they move one by one and the
-// others are 0.  ONCE: data that is read once, which leaves L1 to the weights.
-template <bool WHOLE, bool ONCE, class T>
+// How rows meet vectors: SURE < 0: element by element (rows that are not 16-byte
+// aligned); otherwise in vectors, of which the first SURE of each thread are
+// whole and inside the row, and the others checked (a row's last elements move
+// one by one).  A check a vector is a third of the forward kernel's
+// instructions, so the kernels exist with none, with one and with all checked.
+constexpr int ELEMENTS = -1;
+
+// The first n < VE elements of a row's last vector (all its loads at once: one
+// after the other they held the row up by 2 us).
+template <class T>
+__device__ __forceinline__ uint4 load_last(const T* p, int n) {
+  constexpr int VE = Vec<T>::VE;
+  if constexpr (sizeof(T) == 4) {
+    return make_uint4(n > 0 ? __float_as_uint(p[0]) : 0u, n > 1 ? __float_as_uint(p[1]) : 0u,
+                      n > 2 ? __float_as_uint(p[2]) : 0u, 0u);
+  } else {
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(p);
+    uint32_t e[VE];
+#pragma unroll
+    for (int i = 0; i < VE - 1; ++i) e[i] = i < n ? s[i] : 0u;
+    e[VE - 1] = 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+  }
+}
+template <class T>
+__device__ __forceinline__ void store_last(T* p, const uint4& v, int n) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < n) p[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// VE elements at p, of which the first n are inside the row; the others are 0.
+// ONCE: data that is read once, which leaves L1 to the weights.
+template <bool VECTORS, bool ONCE, class T>
 __device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
   Vec<T> v;
-  if constexpr (WHOLE && ONCE) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.raw.x), "=r"(v.raw.y), "=r"(v.raw.z), "=r"(v.raw.w)
-                 : "l"(p));
-  } else if constexpr (WHOLE) {
-    v.raw = *reinterpret_cast<const uint4*>(p);
-  } else {
+  if constexpr (!VECTORS) {
     f2 f[Vec<T>::VP];
 #pragma unroll
     for (int i = 0; i < Vec<T>::VP; ++i)
       f[i] = f2_of(2 * i < n ? to_f(p[2 * i]) : 0.f, 2 * i + 1 < n ? to_f(p[2 * i + 1]) : 0.f);
     v.set(f);
+  } else if (n >= Vec<T>::VE) {
+    if constexpr (ONCE)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.raw.x), "=r"(v.raw.y), "=r"(v.raw.z), "=r"(v.raw.w)
+                   : "l"(p));
+    else
+      v.raw = *reinterpret_cast<const uint4*>(p);
+  } else {
+    v.raw = load_last(p, n);
   }
   return v;
 }
-template <bool WHOLE, class T>
+template <bool VECTORS, class T>
 __device__ __forceinline__ void store_vec(T* p, const f2 (&f)[Vec<T>::VP], int n) {
-  if constexpr (WHOLE) {
-    Vec<T> v;
-    v.set(f);
-    *reinterpret_cast<uint4*>(p) = v.raw;
-  } else {
+  if constexpr (!VECTORS) {
 #pragma unroll
     for (int i = 0; i < Vec<T>::VP; ++i) {
       const float2 e = f2_get(f[i]);
       if (2 * i < n) p[2 * i] = from_f<T>(e.x);
       if (2 * i + 1 < n) p[2 * i + 1] = from_f<T>(e.y);
     }
+  } else {
+    Vec<T> v;
+    v.set(f);
+    if (n >= Vec<T>::VE)
+      *reinterpret_cast<uint4*>(p) = v.raw;
+    else
+      store_last(p, v.raw, n);
   }
 }
 
 // VE elements of gamma or beta, in fp32 (W32) or in the activations' type.
-template <bool WHOLE, bool W32, class T>
+template <bool VECTORS, bool W32, class T>
 __device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int c, int n) {
   if constexpr (W32 || sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < Vec<T>::VP; k += 2) {
-      f2 q[2];
-      load_vec<WHOLE, false>(static_cast<const float*>(p) + c + 2 * k, n - 2 * k).get(q);
+      f2 q[2] = {0ull, 0ull};
+      if (2 * k < n)
+        load_vec<VECTORS, false>(static_cast<const float*>(p) + c + 2 * k, n - 2 * k).get(q);
       w[k] = q[0];
       w[k + 1] = q[1];
     }
   } else {
-    load_vec<WHOLE, false>(static_cast<const T*>(p) + c, n).get(w);
+    load_vec<VECTORS, false>(static_cast<const T*>(p) + c, n).get(w);
   }
 }
-template <bool WHOLE, class T>
+template <bool VECTORS, class T>
 __device__ __forceinline__ void load_weight(f2 (&w)[Vec<T>::VP], const void* p, int f32, int c, int n) {
-  f32 ? load_weight<WHOLE, true, T>(w, p, c, n) : load_weight<WHOLE, false, T>(w, p, c, n);
+  f32 ? load_weight<VECTORS, true, T>(w, p, c, n) : load_weight<VECTORS, false, T>(w, p, c, n);
 }
 
 // 0 for the elements of a vector past its row's end.
-template <bool WHOLE, int VP>
+template <int VP>
 __device__ __forceinline__ void clear_past(f2 (&v)[VP], int n) {
-  if constexpr (!WHOLE) {
+  if (n >= 2 * VP) return;
 #pragma unroll
-    for (int i = 0; i < VP; ++i) {
-      const float2 e = f2_get(v[i]);
-      v[i] = f2_of(2 * i < n ? e.x : 0.f, 2 * i + 1 < n ? e.y : 0.f);
-    }
+  for (int i = 0; i < VP; ++i) {
+    const float2 e = f2_get(v[i]);
+    v[i] = f2_of(2 * i < n ? e.x : 0.f, 2 * i + 1 < n ? e.y : 0.f);
   }
 }
 
@@ -227,25 +270,20 @@ struct FwdArgs {
   float eps, qscale;
 };
 
-// How rows meet vectors: element by element; in whole vectors (C is a multiple
-// of the vector and every row 16-byte aligned); or so that besides every
-// thread has all of its NV vectors, which saves the checks.
-enum Mode { ELEMENTS = 0, WHOLE_VECTORS = 1, FULL_ROWS = 2 };
-
 // y = (h - mu) rstd gamma + beta of a thread's vectors (v holds h - mu), stored in its type or as int8 codes.
-template <class T, int NV, int MODE, bool W32, bool BETA, bool S8>
+template <class T, int NV, int SURE, bool W32, bool BETA, bool S8>
 __device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::VP], int64_t row, int t, int threads,
                                           f2 r2) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
-  constexpr bool WHOLE = MODE != ELEMENTS, FULL = MODE == FULL_ROWS;
+  constexpr bool VECTORS = SURE >= 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (t + k * threads) * VE;
-    const int n = a.C - c;
-    if (!FULL && n <= 0) continue;
+    const int n = k < SURE ? VE : a.C - c;
+    if (n <= 0) continue;
     f2 g[VP], b[VP];
-    load_weight<WHOLE, W32, T>(g, a.gamma, c, n);
-    if constexpr (BETA) load_weight<WHOLE, W32, T>(b, a.beta, c, n);
+    load_weight<VECTORS, W32, T>(g, a.gamma, c, n);
+    if constexpr (BETA) load_weight<VECTORS, W32, T>(b, a.beta, c, n);
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const f2 z = f2_mul(v[k][i], r2);
@@ -261,7 +299,7 @@ __device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::
         w[i / 4] = (i % 4 ? w[i / 4] : 0u) | (static_cast<uint32_t>(code & 0xFF) << (8 * (i % 4)));
       }
       int8_t* o = static_cast<int8_t*>(a.y) + row * a.ldy + c;
-      if constexpr (WHOLE) {
+      if (VECTORS && n >= VE) {
         if constexpr (VE == 8)
           *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[VE / 4 - 1]);
         else
@@ -272,26 +310,26 @@ __device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::
           if (i < n) o[i] = static_cast<int8_t>(w[i / 4] >> (8 * (i % 4)));
       }
     } else {
-      store_vec<WHOLE>(static_cast<T*>(a.y) + row * a.ldy + c, v[k], n);
+      store_vec<VECTORS>(static_cast<T*>(a.y) + row * a.ldy + c, v[k], n);
     }
   }
 }
 
 // LANES: a row belongs to 2^lg lanes of a warp, otherwise to the block;
 // thread t of the row holds vectors t, t + threads, ... (NV of them).
-template <class T, int NV, int MODE, bool LANES>
+template <class T, int NV, int SURE, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 ? 1 : 2) ln_fwd_kernel(const FwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
-  constexpr bool WHOLE = MODE != ELEMENTS, FULL = MODE == FULL_ROWS;
+  constexpr bool VECTORS = SURE >= 0;
   __shared__ __align__(16) float red[LANES ? 4 : 64];
   const int threads = LANES ? 1 << a.lg : blockDim.x;
   const int t = LANES ? threadIdx.x & (threads - 1) : threadIdx.x;
   int row = blockIdx.x;
   bool live = true;
   if constexpr (LANES) {
-    row = (blockIdx.x * blockDim.x + threadIdx.x) >> a.lg;
-    live = row < a.M;
-    row = live ? row : a.M - 1;  // lanes past the last row follow it and write nothing
+    const int64_t r = int64_t(blockIdx.x) * (blockDim.x >> a.lg) + (threadIdx.x >> a.lg);
+    live = r < a.M;
+    row = live ? int(r) : a.M - 1;  // lanes past the last row follow it and write nothing
   } else {
     for (int i = threadIdx.x; i < 64; i += blockDim.x) red[i] = 0.f;
   }
@@ -303,8 +341,9 @@ __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
+      const int n = k < SURE ? VE : a.C - c;
       Vec<T> e;
-      if (FULL || c < a.C) e = load_vec<WHOLE, true>(x + c, a.C - c);
+      if (n > 0) e = load_vec<VECTORS, true>(x + c, n);
       e.get(v[k]);
     }
   }
@@ -315,16 +354,17 @@ __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (!FULL && c >= a.C) continue;
+      const int n = k < SURE ? VE : a.C - c;
+      if (n <= 0) continue;
       f2 r[VP];
-      load_vec<WHOLE, true>(res + c, a.C - c).get(r);
+      load_vec<VECTORS, true>(res + c, n).get(r);
       // the backward pass reads h as it is stored, so the norm is taken of the rounded sum
       Vec<T> e;
 #pragma unroll
       for (int i = 0; i < VP; ++i) v[k][i] = f2_add(v[k][i], r[i]);
       e.set(v[k]);
       e.get(v[k]);
-      if (live) store_vec<WHOLE>(h + c, v[k], a.C - c);
+      if (live) store_vec<VECTORS>(h + c, v[k], n);
     }
   }
   f2 s = 0ull;
@@ -339,11 +379,11 @@ __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 
   s = 0ull;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int n = a.C - (t + k * threads) * VE;
-    if (!FULL && n <= 0) continue;
+    const int n = k < SURE ? VE : a.C - (t + k * threads) * VE;
+    if (n <= 0) continue;
 #pragma unroll
     for (int i = 0; i < VP; ++i) v[k][i] = f2_add(v[k][i], nmu);
-    clear_past<WHOLE>(v[k], n);
+    clear_past(v[k], n);
 #pragma unroll
     for (int i = 0; i < VP; ++i) s = f2_fma(v[k][i], v[k][i], s);
   }
@@ -358,15 +398,15 @@ __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 
   // one copy of the last step for each kind of weights and output, so that its
   // loop has no branch (they cost a third of the kernel's instructions)
   if (a.s8) {
-    if (a.wf32) a.beta ? ln_finish<T, NV, MODE, true, true, true>(a, v, row, t, threads, r2)
-                       : ln_finish<T, NV, MODE, true, false, true>(a, v, row, t, threads, r2);
-    else a.beta ? ln_finish<T, NV, MODE, false, true, true>(a, v, row, t, threads, r2)
-                : ln_finish<T, NV, MODE, false, false, true>(a, v, row, t, threads, r2);
+    if (a.wf32) a.beta ? ln_finish<T, NV, SURE, true, true, true>(a, v, row, t, threads, r2)
+                       : ln_finish<T, NV, SURE, true, false, true>(a, v, row, t, threads, r2);
+    else a.beta ? ln_finish<T, NV, SURE, false, true, true>(a, v, row, t, threads, r2)
+                : ln_finish<T, NV, SURE, false, false, true>(a, v, row, t, threads, r2);
   } else {
-    if (a.wf32) a.beta ? ln_finish<T, NV, MODE, true, true, false>(a, v, row, t, threads, r2)
-                       : ln_finish<T, NV, MODE, true, false, false>(a, v, row, t, threads, r2);
-    else a.beta ? ln_finish<T, NV, MODE, false, true, false>(a, v, row, t, threads, r2)
-                : ln_finish<T, NV, MODE, false, false, false>(a, v, row, t, threads, r2);
+    if (a.wf32) a.beta ? ln_finish<T, NV, SURE, true, true, false>(a, v, row, t, threads, r2)
+                       : ln_finish<T, NV, SURE, true, false, false>(a, v, row, t, threads, r2);
+    else a.beta ? ln_finish<T, NV, SURE, false, true, false>(a, v, row, t, threads, r2)
+                : ln_finish<T, NV, SURE, false, false, false>(a, v, row, t, threads, r2);
   }
 }
 
@@ -394,7 +434,6 @@ struct BwdRow {
   f2 g[NV][VP], z[NV][VP];
   f2 s1, s2;
   __device__ __forceinline__ void clear() { s1 = s2 = 0ull; }
-  template <bool WHOLE>
   __device__ __forceinline__ void take(int k, const Vec<T>& x, const Vec<T>& dy, const f2 (&ga)[VP], float mu,
                                        float rstd, f2 (&dg)[VP], f2 (&db)[VP], int n) {
     const f2 r2 = f2_of(rstd, rstd), nm = f2_of(-mu, -mu);
@@ -403,7 +442,7 @@ struct BwdRow {
     dy.get(d);
 #pragma unroll
     for (int i = 0; i < VP; ++i) z[k][i] = f2_mul(f2_add(z[k][i], nm), r2);
-    clear_past<WHOLE>(z[k], n);
+    clear_past(z[k], n);
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       g[k][i] = f2_mul(d[i], ga[i]);
@@ -459,7 +498,7 @@ __device__ __forceinline__ void store_part(float* p, int C, int t, int threads, 
 // 2^lg lanes); the columns' sums stay in registers over all of them and go to
 // the block's own rows of `part` at the end, so the order of every sum is
 // fixed.  The next row's loads are issued before this row's sums.
-template <class T, int NV, bool WHOLE, bool LANES>
+template <class T, int NV, bool VECTORS, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
   __shared__ __align__(16) float red[LANES ? 4 : 128];
@@ -478,7 +517,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
     const int c = (t + k * threads) * VE;
 #pragma unroll
     for (int i = 0; i < VP; ++i) ga[k][i] = dg[k][i] = db[k][i] = 0ull;
-    if (c < a.C) load_weight<WHOLE, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+    if (c < a.C) load_weight<VECTORS, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
   }
   const float inv = 1.f / static_cast<float>(a.C);
   const int64_t step = int64_t(gridDim.x) * groups;
@@ -492,8 +531,8 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
       if (c >= a.C) continue;
-      x[k] = load_vec<WHOLE, true>(static_cast<const T*>(a.x) + row * a.ldx + c, a.C - c);
-      dy[k] = load_vec<WHOLE, true>(static_cast<const T*>(a.dy) + row * a.lddy + c, a.C - c);
+      x[k] = load_vec<VECTORS, true>(static_cast<const T*>(a.x) + row * a.ldx + c, a.C - c);
+      dy[k] = load_vec<VECTORS, true>(static_cast<const T*>(a.dy) + row * a.lddy + c, a.C - c);
     }
   };
   const int64_t first = int64_t(blockIdx.x) * groups;
@@ -509,7 +548,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int n = a.C - (t + k * threads) * VE;
-        if (n > 0) r.template take<WHOLE>(k, x[k], dy[k], ga[k], mu, rstd, dg[k], db[k], n);
+        if (n > 0) r.take(k, x[k], dy[k], ga[k], mu, rstd, dg[k], db[k], n);
       }
     }
     fetch(row + step);
@@ -531,9 +570,9 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
       f2 h[VP];
 #pragma unroll
       for (int i = 0; i < VP; ++i) h[i] = 0ull;
-      if (a.dh) load_vec<WHOLE, true>(static_cast<const T*>(a.dh) + row * a.lddh + c, n).get(h);
+      if (a.dh) load_vec<VECTORS, true>(static_cast<const T*>(a.dh) + row * a.lddh + c, n).get(h);
       r.give(k, s1 * inv, s2 * inv, rstd, h, h);
-      store_vec<WHOLE>(static_cast<T*>(a.dx) + row * a.lddx + c, h, n);
+      store_vec<VECTORS>(static_cast<T*>(a.dx) + row * a.lddx + c, h, n);
     }
   }
   if constexpr (LANES) {
@@ -560,7 +599,7 @@ __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdA
 // stage is free at the barrier of its own sums; with four, which would not
 // fit, it is read from the ring twice, and gamma with it, and the stage is free
 // at the next row's barrier.
-template <class T, int NV, bool FULL, bool DH>
+template <class T, int NV, int SURE, bool DH>
 __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -568,7 +607,8 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
   __shared__ uint64_t full[16];
   const int threads = blockDim.x, t = threadIdx.x;
   for (int i = t; i < 64; i += threads) red[0][0][i] = 0.f;
-  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T);
+  // whole vectors come through the ring; a row's last elements are read directly
+  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T) / 16 * 16;
   const uint32_t stage_bytes = row_bytes * (DH ? 3 : 2);
   if (t == 0) {
     for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
@@ -600,7 +640,7 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
       if constexpr (kHold) ga[k][i] = 0ull;
     }
     if constexpr (kHold) {
-      if (FULL || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+      if (k < SURE || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, k < SURE ? VE : a.C - c);
     }
   }
   const float inv = 1.f / static_cast<float>(a.C);
@@ -618,23 +658,28 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
     BwdRow<T, NH> r;
     r.clear();
     Vec<T> dh[NH];
-    auto read = [&](int c, Vec<T>& x, Vec<T>& dy) {
-      x.raw = *reinterpret_cast<const uint4*>(from + c * sizeof(T));
-      dy.raw = *reinterpret_cast<const uint4*>(from + row_bytes + c * sizeof(T));
+    // vector c of x, dy or dh (the i-th part of the stage)
+    auto read = [&](int i, const void* p, int64_t ld, int c, int n) {
+      Vec<T> v;
+      if (n >= VE)
+        v.raw = *reinterpret_cast<const uint4*>(from + i * row_bytes + c * sizeof(T));
+      else
+        v.raw = load_last(static_cast<const T*>(p) + row * ld + c, n);
+      return v;
     };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (!FULL && c >= a.C) continue;
+      const int n = k < SURE ? VE : a.C - c;
+      if (n <= 0) continue;
       const int kh = kHold ? k : 0;
-      Vec<T> x, dy;
-      read(c, x, dy);
+      const Vec<T> x = read(0, a.x, a.ldx, c, n), dy = read(1, a.dy, a.lddy, c, n);
       if constexpr (kHold) {
-        if (DH) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+        if (DH) dh[k] = read(2, a.dh, a.lddh, c, n);
       } else {
-        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
+        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, n);
       }
-      r.template take<true>(kh, x, dy, ga[kh], mu, rstd, dg[k], db[k], VE);
+      r.take(kh, x, dy, ga[kh], mu, rstd, dg[k], db[k], n);
     }
     const float mc = mu, rs = rstd;
     if (row + step < a.M) {
@@ -657,7 +702,8 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (t + k * threads) * VE;
-      if (!FULL && c >= a.C) continue;
+      const int n = k < SURE ? VE : a.C - c;
+      if (n <= 0) continue;
       f2 h[VP];
 #pragma unroll
       for (int i = 0; i < VP; ++i) h[i] = 0ull;
@@ -665,17 +711,16 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
         if (DH) dh[k].get(h);
         r.give(k, m1, m2, rs, h, h);
       } else {
-        Vec<T> x, dy;
-        read(c, x, dy);
+        const Vec<T> x = read(0, a.x, a.ldx, c, n), dy = read(1, a.dy, a.lddy, c, n);
         if (DH) {
-          dh[0].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
+          dh[0] = read(2, a.dh, a.lddh, c, n);
           dh[0].get(h);
         }
-        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, a.C - c);
+        load_weight<true, T>(ga[0], a.gamma, a.wf32, c, n);
         r.again(x, dy, ga[0], mc, rs);
         r.give(0, m1, m2, rs, h, h);
       }
-      store_vec<true>(dx + c, h, VE);
+      store_vec<true>(dx + c, h, n);
     }
     if (++s == a.stages) {
       s = 0;
@@ -689,13 +734,14 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const BwdArgs a) {
 // warp has its own ring, and the warps' column sums are added in their order
 // at the end.  A row of 768 fp16 values took the block kernel 1.5 us a block.
 constexpr int bwd_warps(int es, int nv) { return es == 4 || nv == 2 ? 16 : 8; }  // what the registers allow
-template <class T, int NV, bool FULL, bool DH>
+template <class T, int NV, int SURE, bool DH>
 __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_kernel(const BwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP, kBwdWarps = bwd_warps(sizeof(T), NV);
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[kBwdWarps][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T);
+  // whole vectors come through the ring; a row's last elements are read directly
+  const uint32_t row_bytes = uint32_t(a.C) * sizeof(T) / 16 * 16;
   const uint32_t stage_bytes = row_bytes * (DH ? 3 : 2);
   uint8_t* ring = smem + size_t(warp) * a.stages * stage_bytes;
   uint64_t* full = bars[warp];
@@ -724,7 +770,7 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_ker
     const int c = (lane + 32 * k) * VE;
 #pragma unroll
     for (int i = 0; i < VP; ++i) ga[k][i] = dg[k][i] = db[k][i] = 0ull;
-    if (FULL || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, a.C - c);
+    if (k < SURE || c < a.C) load_weight<true, T>(ga[k], a.gamma, a.wf32, c, k < SURE ? VE : a.C - c);
   }
   const float inv = 1.f / static_cast<float>(a.C);
   int s = 0;
@@ -738,18 +784,26 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_ker
   for (int64_t row = first; row < a.M; row += step) {
     mbar_wait(&full[s], phase, &never, a.err, ERR_WAIT_FULL);
     const uint8_t* from = ring + s * stage_bytes;
+    // vector c of x, dy or dh (the i-th part of the stage)
+    auto read = [&](int i, const void* p, int64_t ld, int c, int n) {
+      Vec<T> v;
+      if (n >= VE)
+        v.raw = *reinterpret_cast<const uint4*>(from + i * row_bytes + c * sizeof(T));
+      else
+        v.raw = load_last(static_cast<const T*>(p) + row * ld + c, n);
+      return v;
+    };
     BwdRow<T, NV> r;
     r.clear();
     Vec<T> dh[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (lane + 32 * k) * VE;
-      if (!FULL && c >= a.C) continue;
-      Vec<T> x, dy;
-      x.raw = *reinterpret_cast<const uint4*>(from + c * sizeof(T));
-      dy.raw = *reinterpret_cast<const uint4*>(from + row_bytes + c * sizeof(T));
-      if (DH) dh[k].raw = *reinterpret_cast<const uint4*>(from + 2 * row_bytes + c * sizeof(T));
-      r.template take<true>(k, x, dy, ga[k], mu, rstd, dg[k], db[k], VE);
+      const int n = k < SURE ? VE : a.C - c;
+      if (n <= 0) continue;
+      const Vec<T> x = read(0, a.x, a.ldx, c, n), dy = read(1, a.dy, a.lddy, c, n);
+      if (DH) dh[k] = read(2, a.dh, a.lddh, c, n);
+      r.take(k, x, dy, ga[k], mu, rstd, dg[k], db[k], n);
     }
     const float rs = rstd;
     if (row + step < a.M) {
@@ -764,13 +818,14 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_ker
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (lane + 32 * k) * VE;
-      if (!FULL && c >= a.C) continue;
+      const int n = k < SURE ? VE : a.C - c;
+      if (n <= 0) continue;
       f2 h[VP];
 #pragma unroll
       for (int i = 0; i < VP; ++i) h[i] = 0ull;
       if (DH) dh[k].get(h);
       r.give(k, m1, m2, rs, h, h);
-      store_vec<true>(dx + c, h, VE);
+      store_vec<true>(dx + c, h, n);
     }
     if (++s == a.stages) {
       s = 0;
@@ -850,12 +905,11 @@ Shape fwd_shape(int C, int es) {
 }
 
 // One vector a lane where that holds the row (several rows a warp where it is
-// shorter); a warp with up to four a lane where the rows are whole vectors;
-// otherwise one to four vectors a thread of a block.
+// shorter); a warp with up to four a lane; otherwise one to four vectors a thread of a block.
 Shape bwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
   if (nvec <= 32) return {true, lg_of(nvec), 1, 256};
-  if (nvec <= 128 && (C * es) % 16 == 0) {
+  if (nvec <= 128) {
     const int nv = (nvec + 31) / 32;
     return {true, 5, nv, 32 * bwd_warps(es, nv)};
   }
@@ -875,69 +929,86 @@ int bwd_blocks(int64_t M, const Shape& s) {
   return static_cast<int>(work < cap ? work : cap);
 }
 
-template <class T, int MODE>
-cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, int64_t blocks, cudaStream_t st) {
-  void (*k)(const FwdArgs) = !s.lanes    ? ln_fwd_kernel<T, 4, MODE, false>
-                             : s.nv == 1 ? ln_fwd_kernel<T, 1, MODE, true>
-                             : s.nv == 2 ? ln_fwd_kernel<T, 2, MODE, true>
-                             : s.nv == 3 ? ln_fwd_kernel<T, 3, MODE, true>
-                                         : ln_fwd_kernel<T, 4, MODE, true>;
+// The vectors of each thread that are whole and inside the row: all `nv`, all
+// but the last, or (0) none to be sure of.
+int sure_vectors(const Shape& s, int C, int es) {
+  const int threads = s.lanes ? 1 << s.lg : s.threads, whole = C * es / 16;
+  return whole >= threads * s.nv && C * es % 16 == 0 ? s.nv : whole >= threads * (s.nv - 1) ? s.nv - 1 : 0;
+}
+
+using FwdKernel = void (*)(const FwdArgs);
+template <class T, int NV, bool LANES>
+FwdKernel fwd_kernel(int sure) {
+  return sure == NV       ? ln_fwd_kernel<T, NV, NV, LANES>
+         : sure < 0       ? ln_fwd_kernel<T, NV, ELEMENTS, LANES>
+         : sure == NV - 1 ? ln_fwd_kernel<T, NV, NV - 1, LANES>
+                          : ln_fwd_kernel<T, NV, 0, LANES>;
+}
+
+template <class T>
+cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, bool vectors, int64_t blocks, cudaStream_t st) {
+  const int sure = vectors ? sure_vectors(s, a.C, sizeof(T)) : ELEMENTS;
+  const FwdKernel k = !s.lanes    ? fwd_kernel<T, 4, false>(sure)
+                      : s.nv == 1 ? fwd_kernel<T, 1, true>(sure)
+                      : s.nv == 2 ? fwd_kernel<T, 2, true>(sure)
+                      : s.nv == 3 ? fwd_kernel<T, 3, true>(sure)
+                                  : fwd_kernel<T, 4, true>(sure);
   return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), 0, st, a);
 }
 
-// Every thread of a row has all of its vectors.
-bool full_rows(const Shape& s, int C, int es) { return (s.lanes ? 1 << s.lg : s.threads) * s.nv * 16 == C * es; }
-
 using BwdKernel = void (*)(const BwdArgs);
 template <class T, int NV>
-BwdKernel ring_kernel(bool full, bool dh) {
-  return full ? (dh ? ln_bwd_ring_kernel<T, NV, true, true> : ln_bwd_ring_kernel<T, NV, true, false>)
-              : (dh ? ln_bwd_ring_kernel<T, NV, false, true> : ln_bwd_ring_kernel<T, NV, false, false>);
+BwdKernel ring_kernel(int sure, bool dh) {
+  return sure == NV       ? (dh ? ln_bwd_ring_kernel<T, NV, NV, true> : ln_bwd_ring_kernel<T, NV, NV, false>)
+         : sure == NV - 1 ? (dh ? ln_bwd_ring_kernel<T, NV, NV - 1, true> : ln_bwd_ring_kernel<T, NV, NV - 1, false>)
+                          : (dh ? ln_bwd_ring_kernel<T, NV, 0, true> : ln_bwd_ring_kernel<T, NV, 0, false>);
 }
 template <class T, int NV>
-BwdKernel warp_kernel(bool full, bool dh) {
-  return full ? (dh ? ln_bwd_warp_kernel<T, NV, true, true> : ln_bwd_warp_kernel<T, NV, true, false>)
-              : (dh ? ln_bwd_warp_kernel<T, NV, false, true> : ln_bwd_warp_kernel<T, NV, false, false>);
+BwdKernel warp_kernel(int sure, bool dh) {  // a warp's rows fill all but the last vector of a lane
+  return sure == NV ? (dh ? ln_bwd_warp_kernel<T, NV, NV, true> : ln_bwd_warp_kernel<T, NV, NV, false>)
+                    : (dh ? ln_bwd_warp_kernel<T, NV, NV - 1, true> : ln_bwd_warp_kernel<T, NV, NV - 1, false>);
 }
 
-template <class T, bool WHOLE>
-cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, int blocks, cudaStream_t st) {
-  const bool full = full_rows(s, a.C, sizeof(T)), dh = a.dh != nullptr;
+template <class T>
+cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, bool vectors, int blocks, cudaStream_t st) {
+  const int sure = sure_vectors(s, a.C, sizeof(T));
+  const bool dh = a.dh != nullptr;
+  const int64_t row = int64_t(a.C) * sizeof(T) / 16 * 16 * (dh ? 3 : 2);  // bytes of a row in a ring
   BwdKernel k;
   size_t smem = 0;
   BwdArgs b = a;
   if (s.lanes && s.nv == 1) {
-    k = ln_bwd_kernel<T, 1, WHOLE, true>;
+    k = vectors ? ln_bwd_kernel<T, 1, true, true> : ln_bwd_kernel<T, 1, false, true>;
     smem = size_t(s.threads) * 2 * Vec<T>::VE * sizeof(float);
+  } else if (s.lanes && !vectors) {  // the block kernel, with the warp kernel's blocks
+    Shape q = s;
+    q.lanes = false;
+    q.nv = 1;
+    q.threads = round32((a.C * int(sizeof(T)) + 15) / 16);
+    return launch_bwd<T>(a, q, false, blocks, st);
   } else if (s.lanes) {
-    if constexpr (WHOLE) {
-      // one block an SM; two stages of the longest rows (2 KB) take 16 * 2 * 6 KB
-      const int64_t stage = int64_t(a.C) * sizeof(T) * (dh ? 3 : 2) * (s.threads / 32);
-      const int64_t stages = 200 * 1024 / stage;
-      b.stages = stages > 8 ? 8 : static_cast<int>(stages);
-      const int64_t sums = int64_t(s.threads / 32) * 2 * a.C * 4;
-      smem = size_t(b.stages * stage > sums ? b.stages * stage : sums);
-      k = s.nv == 2 ? warp_kernel<T, 2>(full, dh) : s.nv == 3 ? warp_kernel<T, 3>(full, dh) : warp_kernel<T, 4>(full, dh);
-    } else {  // rows of whole vectors that are not 16-byte aligned: the block kernel
-      Shape q = s;
-      q.lanes = false;
-      q.nv = 1;
-      q.threads = round32((a.C * int(sizeof(T)) + 15) / 16);
-      return launch_bwd<T, false>(a, q, blocks, st);
-    }
+    // one block an SM; two stages of the longest rows (2 KB) take 16 * 2 * 6 KB
+    const int64_t stage = row * (s.threads / 32);
+    const int64_t stages = 200 * 1024 / stage;
+    b.stages = stages > 8 ? 8 : static_cast<int>(stages);
+    const int64_t sums = int64_t(s.threads / 32) * 2 * a.C * 4;
+    smem = size_t(b.stages * stage > sums ? b.stages * stage : sums);
+    k = s.nv == 2 ? warp_kernel<T, 2>(sure, dh) : s.nv == 3 ? warp_kernel<T, 3>(sure, dh) : warp_kernel<T, 4>(sure, dh);
   } else {
-    k = s.nv == 1   ? ln_bwd_kernel<T, 1, WHOLE, false>
-        : s.nv == 2 ? ln_bwd_kernel<T, 2, WHOLE, false>
-                    : ln_bwd_kernel<T, 4, WHOLE, false>;
-    if constexpr (WHOLE) {
-      // the ring, where at least two rows of it fit the block's share of shared memory
-      const int64_t stage = int64_t(a.C) * sizeof(T) * (dh ? 3 : 2);
-      const int64_t stages = (224 * 1024 / bwd_per_sm(s) - 1024) / stage;
-      if (s.threads <= 512 && stages >= 2) {
-        b.stages = stages > 16 ? 16 : static_cast<int>(stages);
-        smem = size_t(b.stages * stage);
-        k = s.nv == 1 ? ring_kernel<T, 1>(full, dh) : s.nv == 2 ? ring_kernel<T, 2>(full, dh) : ring_kernel<T, 4>(full, dh);
-      }
+    // the ring, where at least two rows of it fit the block's share of shared memory
+    const int64_t stages = (224 * 1024 / bwd_per_sm(s) - 1024) / row;
+    if (vectors && s.threads <= 512 && stages >= 2) {
+      b.stages = stages > 16 ? 16 : static_cast<int>(stages);
+      smem = size_t(b.stages * row);
+      k = s.nv == 1   ? ring_kernel<T, 1>(sure, dh)
+          : s.nv == 2 ? ring_kernel<T, 2>(sure, dh)
+                      : ring_kernel<T, 4>(sure, dh);
+    } else if (vectors) {  // 32-bit rows of more than 8192 columns
+      k = ln_bwd_kernel<T, 4, true, false>;
+    } else {
+      k = s.nv == 1   ? ln_bwd_kernel<T, 1, false, false>
+          : s.nv == 2 ? ln_bwd_kernel<T, 2, false, false>
+                      : ln_bwd_kernel<T, 4, false, false>;
     }
   }
   if (smem > 40 * 1024) {  // 48 KB with the static arrays
@@ -973,23 +1044,12 @@ spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void*
                   ldh, ldy, int(M), int(C), s.lg,  wdtype == SPG_F32, s8,   eps,  qscale};
   const int64_t rows = s.lanes ? s.threads >> s.lg : 1;
   const int64_t blocks = (M + rows - 1) / rows;
-  // whole 16-byte vectors in rows that start on 16-byte boundaries; otherwise element by element
-  const bool al = (C * es) % 16 == 0 && vec_ok(X, ldx, es) && vec_ok(res, ldres, es) && vec_ok(H, ldh, es) &&
+  // vectors in rows that start on 16-byte boundaries; otherwise element by element
+  const bool al = vec_ok(X, ldx, es) && vec_ok(res, ldres, es) && vec_ok(H, ldh, es) &&
                   (s8 ? aligned(Y, 8) && ldy % 8 == 0 : vec_ok(Y, ldy, es)) && aligned(gamma, 16) && aligned(beta, 16);
-  const int mode = !al ? ELEMENTS : full_rows(s, int(C), es) ? FULL_ROWS : WHOLE_VECTORS;
-  cudaError_t e;
-  if (dtype == SPG_F32)
-    e = mode == ELEMENTS        ? launch_fwd<float, ELEMENTS>(b, s, blocks, st)
-        : mode == WHOLE_VECTORS ? launch_fwd<float, WHOLE_VECTORS>(b, s, blocks, st)
-                                : launch_fwd<float, FULL_ROWS>(b, s, blocks, st);
-  else if (dtype == SPG_F16)
-    e = mode == ELEMENTS        ? launch_fwd<__half, ELEMENTS>(b, s, blocks, st)
-        : mode == WHOLE_VECTORS ? launch_fwd<__half, WHOLE_VECTORS>(b, s, blocks, st)
-                                : launch_fwd<__half, FULL_ROWS>(b, s, blocks, st);
-  else
-    e = mode == ELEMENTS        ? launch_fwd<__nv_bfloat16, ELEMENTS>(b, s, blocks, st)
-        : mode == WHOLE_VECTORS ? launch_fwd<__nv_bfloat16, WHOLE_VECTORS>(b, s, blocks, st)
-                                : launch_fwd<__nv_bfloat16, FULL_ROWS>(b, s, blocks, st);
+  const cudaError_t e = dtype == SPG_F32   ? launch_fwd<float>(b, s, al, blocks, st)
+                        : dtype == SPG_F16 ? launch_fwd<__half>(b, s, al, blocks, st)
+                                           : launch_fwd<__nv_bfloat16>(b, s, al, blocks, st);
   return e == cudaSuccess ? launch_status() : SPG_ERR_CUDA;
 }
 
@@ -1047,14 +1107,11 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
     if (!err) return SPG_ERR_CUDA;
     const BwdArgs a{dY,  X,    dH,   dX,     gamma,  mean, rstd, static_cast<float*>(workspace), lddy,
                     ldx, lddh, lddx, int(M), int(C), s.lg, wdtype == SPG_F32, 0, err};
-    const bool al = (C * es) % 16 == 0 && vec_ok(dY, lddy, es) && vec_ok(X, ldx, es) && vec_ok(dH, lddh, es) && vec_ok(dX, lddx, es) &&
+    const bool al = vec_ok(dY, lddy, es) && vec_ok(X, ldx, es) && vec_ok(dH, lddh, es) && vec_ok(dX, lddx, es) &&
                     aligned(gamma, 16);
-    cudaError_t e;
-    if (dtype == SPG_F32) e = al ? launch_bwd<float, true>(a, s, blocks, st) : launch_bwd<float, false>(a, s, blocks, st);
-    else if (dtype == SPG_F16)
-      e = al ? launch_bwd<__half, true>(a, s, blocks, st) : launch_bwd<__half, false>(a, s, blocks, st);
-    else
-      e = al ? launch_bwd<__nv_bfloat16, true>(a, s, blocks, st) : launch_bwd<__nv_bfloat16, false>(a, s, blocks, st);
+    const cudaError_t e = dtype == SPG_F32   ? launch_bwd<float>(a, s, al, blocks, st)
+                          : dtype == SPG_F16 ? launch_bwd<__half>(a, s, al, blocks, st)
+                                             : launch_bwd<__nv_bfloat16>(a, s, al, blocks, st);
     if (e != cudaSuccess) return SPG_ERR_CUDA;
   }
   // no rows: the sums over them are zero
