@@ -150,11 +150,12 @@ def _ptr(t) -> Optional[int]:
 
 def _on_device(t, name: str) -> None:
     """A tensor whose pointer goes to a kernel lives on the current CUDA device."""
-    import torch
+    torch = _tm()
+    if t.is_cuda and t.get_device() == torch.cuda.current_device():
+        return
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (it is on {t.device})")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _arg(t, name: str, dtypes, shape=None, contiguous=False, optional=False):
@@ -527,11 +528,15 @@ def _like(t, name: str, dtype, shape, dev: int) -> int:
 
 def _first(t, name: str, dtypes, dims: int = 2) -> int:
     """_arg for a call's first tensor; returns its row pitch."""
-    if not isinstance(t, _tm().Tensor) or t.dtype not in dtypes:
+    if not isinstance(t, _tm().Tensor) or t.dtype not in dtypes or t.dim() != dims:
         _arg(t, name, dtypes)
-    if t.dim() != dims:
         raise ValueError(f"{name} must be {dims}-D")
     _on_device(t, name)
+    if dims == 2:
+        ld, unit = t.stride()
+        M, C = t.shape
+        if unit == 1 or C <= 1 or not M:
+            return ld if M > 1 else (C + 15) // 16 * 16
     return _like(t, name, t.dtype, t.shape, t.get_device())
 
 
@@ -597,13 +602,15 @@ def _ln_fwd(fn, X, gamma, beta, eps, qscale, residual, H, Y, ydt, stats, stream)
         res = residual.data_ptr()
         if H is None:
             H = _new(shape, dt, X, stream, pad=True)
-        ldh = _like(H, "H", dt, shape, dev)
+            ldh = H.stride(0)
+        else:
+            ldh = _like(H, "H", dt, shape, dev)
         h = H.data_ptr()
     elif H is not None:
         raise ValueError("H is the sum of X and residual: it needs a residual")
     if Y is None:
         Y = _new(shape, ydt, X, stream, pad=True)
-        ldy = _like(Y, "Y", ydt, shape, dev)
+        ldy = Y.stride(0)
     else:
         ldy = _like(Y, "Y", ydt, shape, dev)
         _apart(Y=Y, H=H)
@@ -649,7 +656,9 @@ def layernorm_bwd(dY, X, mean, rstd, gamma, dH=None, dX=None, dgamma=None, dbeta
     given = not (dX is None and dgamma is None and dbeta is None and workspace is None)
     if dX is None:
         dX = _new(shape, dt, X, stream, pad=True)
-    lddx = _like(dX, "dX", dt, shape, dev)
+        lddx = dX.stride(0)
+    else:
+        lddx = _like(dX, "dX", dt, shape, dev)
     dgamma = _new((C,), wdt, gamma, stream) if dgamma is None else dgamma
     dbeta = _new((C,), wdt, gamma, stream) if dbeta is None else dbeta
     need = lib().layernorm_bwd_workspace_size(M, C, code)
@@ -727,9 +736,14 @@ def lora_f16(X, A, B, plan: LoraPlan, scale=None, base=None, Y=None, V=None, str
     given = not (Y is None and V is None)
     if V is None:
         V = _new((M, R), dt, X, stream)
+        ldv = V.stride(0)
+    else:
+        ldv = _like(V, "V", dt, (M, R), dev)
     if Y is None:
-        Y = _new((M, N), dt, X, stream, pad=True)
-    ldv, ldy = _like(V, "V", dt, (M, R), dev), _like(Y, "Y", dt, (M, N), dev)
+        Y = _new((M, N), dt, X if base is None else base, stream, pad=True)
+        ldy = Y.stride(0)
+    else:
+        ldy = _like(Y, "Y", dt, (M, N), dev)
     if given:
         _apart(Y=Y, V=V)
     _check("lora_f16", lib().lora_f16(
@@ -756,11 +770,13 @@ def lora_f16_bwd(dY, X, V, A, B, plan: LoraPlan, scale=None, dbase=None, dX=None
     if need_dx:
         if dX is None:
             dX = _new((M, K), dt, X, stream)
-        lddx = _like(dX, "dX", dt, (M, K), dev)
+            lddx = dX.stride(0)
+        else:
+            lddx = _like(dX, "dX", dt, (M, K), dev)
     if dA is None:
-        dA = _new((L, R, K), dt, X, stream)
+        dA = _new((L, R, K), dt, A, stream)
     if dB is None:
-        dB = _new((L, N, R), dt, X, stream)
+        dB = _new((L, N, R), dt, B, stream)
     need = lib().lora_bwd_workspace_size(M, N, K, R, L)
     if workspace is None:
         workspace = _new((need,), _torch.uint8, X, stream)

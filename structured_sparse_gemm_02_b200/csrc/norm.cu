@@ -905,7 +905,7 @@ Shape fwd_shape(int C, int es) {
 }
 
 // One vector a lane where that holds the row (several rows a warp where it is
-// shorter); a warp with up to four a lane; otherwise one to four vectors a thread of a block.
+// shorter); a warp with up to four a lane; otherwise two or four vectors a thread of a block.
 Shape bwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
   if (nvec <= 32) return {true, lg_of(nvec), 1, 256};
@@ -913,14 +913,14 @@ Shape bwd_shape(int C, int es) {
     const int nv = (nvec + 31) / 32;
     return {true, 5, nv, 32 * bwd_warps(es, nv)};
   }
-  const int nv = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+  const int nv = nvec <= 1024 ? 2 : 4;
   return {false, 0, nv, round32((nvec + nv - 1) / nv)};
 }
 
 // Blocks of the backward kernel: as many as are resident, so that each leaves
 // one row of partial sums and no more, and a row group each at least.
 int bwd_per_sm(const Shape& s) {
-  return s.lanes ? (s.nv == 1 ? 3 : 1) : s.threads > 256 ? 1 : s.nv > 1 ? 2 : s.threads > 128 ? 4 : 8;
+  return s.lanes ? (s.nv == 1 ? 3 : 1) : s.threads > 256 ? 1 : s.threads > 128 ? 2 : 4;
 }
 int bwd_blocks(int64_t M, const Shape& s) {
   const int64_t groups = s.lanes ? s.threads >> s.lg : 1;
@@ -1000,9 +1000,7 @@ cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, bool vectors, int block
     if (vectors && s.threads <= 512 && stages >= 2) {
       b.stages = stages > 16 ? 16 : static_cast<int>(stages);
       smem = size_t(b.stages * row);
-      k = s.nv == 1   ? ring_kernel<T, 1>(sure, dh)
-          : s.nv == 2 ? ring_kernel<T, 2>(sure, dh)
-                      : ring_kernel<T, 4>(sure, dh);
+      k = s.nv == 2 ? ring_kernel<T, 2>(sure, dh) : ring_kernel<T, 4>(sure, dh);
     } else if (vectors) {  // 32-bit rows of more than 8192 columns
       k = ln_bwd_kernel<T, 4, true, false>;
     } else {
