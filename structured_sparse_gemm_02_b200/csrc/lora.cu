@@ -750,14 +750,16 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 1 ? 4 : 2) expand
 }
 
 // ---- expand for larger R: the same with tcgen05 ------------------------------------------
-// One block a tile and 128 columns.  The product comes from one MMA chain over
-// R (with mma.sync the operands' traffic through L1 grows with R: 198 us for
-// [8192, 16384] at R = 64, 300 us at R = 128); base is read into registers
-// before it and added in the same layout, which tcgen05.ld 16x256b and a
-// permuted order of G's columns in shared memory give: a lane has 8
-// consecutive columns of a row.
+// A block takes a tile and `span` blocks of 128 columns.  The product comes from
+// one MMA chain over R (with mma.sync the operands' traffic through L1 grows
+// with R: 198 us for [8192, 16384] at R = 64, 300 us at R = 128); base is in
+// registers before it and is added in the same layout, which tcgen05.ld
+// 16x256b and a permuted order of G's columns in shared memory give: a lane has
+// 8 consecutive columns of a row.  P is staged once a block; base of the next
+// columns is read as the registers of this one's become free.
 struct ExpandTcArgs {
   ExpandRegArgs a;
+  int span;
   uint32_t* err;
 };
 constexpr int kTcCols = 128;
@@ -770,9 +772,10 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
   const int R = a.R, Rn = round16(R), halves = R > 64 ? 2 : 1;
-  uint8_t* Ps = smem;                           // [128 rows][R], K-major
-  uint8_t* Gs = Ps + halves * kTile * 128;      // [128 columns][R], K-major, or [R][2 x 64 columns], N-major
-  const Ring ring = ring_at(Gs + (GMN ? 2 * Rn * 128 : halves * kTcCols * 128));
+  const int gbytes = GMN ? 2 * Rn * 128 : halves * kTcCols * 128;
+  uint8_t* Ps = smem;                       // [128 rows][R], K-major
+  uint8_t* Gs = Ps + halves * kTile * 128;  // [128 columns][R], K-major, or [R][2 x 64 columns], N-major
+  const Ring ring = ring_at(Gs + gbytes);
   ring_init(ring, kTcCols, warp);
   const uint32_t tmem = *ring.tmem;
   griddep_wait();
@@ -783,8 +786,8 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
     if (warp == 1) tmem_dealloc(tmem, kTcCols);
     return;
   }
-  const int n0 = blockIdx.x * kTcCols;
-  const int c0 = n0 + 8 * q;  // this lane's columns: c0 .. of each 32
+  const int first = blockIdx.x * ta.span * kTcCols;
+  const int last = min(a.C, first + ta.span * kTcCols);
   int rows[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -792,26 +795,22 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
     rows[k] = r < count ? a.plan.perm[pos + r] : -1;
   }
   uint4 x[4][4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
+  auto fetch = [&](int n0, int h) {  // this lane's columns 8 q .. of 32 h ..
+    const int c = n0 + 32 * h + 8 * q;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x[h][k] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.base && rows[k] >= 0 && c0 + 32 * h < a.C)
-        x[h][k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c0 + 32 * h, a.C);
+      if (a.base && rows[k] >= 0 && c < last) x[h][k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c, a.C);
     }
-  if (!none) {
-    // operands in 128-byte swizzled rows of 64: piece c of row r sits at c ^ (r % 8).
-    // All copies are under way before any is waited for: with loads and stores
-    // through registers R = 64 took 182 us.
-    const int pieces = Rn / 8;
-    for (int i = threadIdx.x; i < count * pieces; i += 128) {
-      const int r = i / pieces, c = i - r * pieces;
-      const bool ok = 8 * c < R;
-      cp_async16(Ps + (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                 a.P + int64_t(a.plan.perm[pos + r]) * a.ldp + (ok ? 8 * c : 0), ok);
-    }
-    const uint16_t* G = a.G + int64_t(adapter) * a.C * R;
+  };
+#pragma unroll
+  for (int h = 0; h < 4; ++h) fetch(first, h);
+  // Operands in 128-byte swizzled rows of 64: piece c of row r sits at c ^ (r % 8).
+  // All copies are under way before any is waited for: with loads and stores
+  // through registers R = 64 took 182 us.
+  const int pieces = Rn / 8;
+  const uint16_t* G = a.G + int64_t(none ? 0 : adapter) * a.C * R;
+  auto stage = [&](int n0) {
     // column 32 i + 8 j + 2 k + e of the MMA is column 32 i + 8 k + 2 j + e of G
     if constexpr (GMN) {
       for (int i = threadIdx.x; i < Rn * (kTcCols / 2); i += 128) {  // pairs of columns
@@ -830,29 +829,48 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
                    G + (ok ? int64_t(n0 + v) * R + 8 * c : 0), ok);
       }
     }
-    cp_async_wait_all();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const uint32_t idesc = instr_desc_major(BF16, kTile, kTcCols, 0, GMN ? 1 : 0);
-      for (int k = 0; k < Rn / 16; ++k) {
-        const uint64_t ad = desc_k_major(Ps + (k >> 2) * kTile * 128) + ((32 * (k & 3)) >> 4);
-        const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, Rn * 128)
-                                : desc_k_major(Gs + (k >> 2) * kTcCols * 128) + ((32 * (k & 3)) >> 4);
-        tc_mma(tmem, ad, bd, idesc, k != 0);
-      }
-      tc_commit(ring.done);
+  };
+  if (!none) {
+    for (int i = threadIdx.x; i < count * pieces; i += 128) {
+      const int r = i / pieces, c = i - r * pieces;
+      const bool ok = 8 * c < R;
+      cp_async16(Ps + (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                 a.P + int64_t(a.plan.perm[pos + r]) * a.ldp + (ok ? 8 * c : 0), ok);
     }
-    __syncwarp();
-    tail_wait(ring.done, 0, ta.err);
-    __syncwarp();
-    tc_fence_after();
+    stage(first);
   }
   const float scale = none ? 0.f : a.scale ? a.scale[adapter] : 1.f;
-  if (32 * warp < count) {
+  const uint32_t idesc = instr_desc_major(BF16, kTile, kTcCols, 0, GMN ? 1 : 0);
+  uint32_t phase = 0;
+  for (int n0 = first; n0 < last; n0 += kTcCols) {
+    const bool more = n0 + kTcCols < last;
+    if (!none) {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();  // operands are there, and the accumulators of the last columns have been read
+      tc_fence_after();
+      if (threadIdx.x == 0) {
+        for (int k = 0; k < Rn / 16; ++k) {
+          const uint64_t ad = desc_k_major(Ps + (k >> 2) * kTile * 128) + ((32 * (k & 3)) >> 4);
+          const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, Rn * 128)
+                                  : desc_k_major(Gs + (k >> 2) * kTcCols * 128) + ((32 * (k & 3)) >> 4);
+          tc_mma(tmem, ad, bd, idesc, k != 0);
+        }
+        tc_commit(ring.done);
+      }
+      __syncwarp();
+      tail_wait(ring.done, phase, ta.err);
+      phase ^= 1u;
+      __syncwarp();
+      tc_fence_after();
+      // the product has read G: the next one is copied behind the sums (a second
+      // buffer costs a block an SM: 159 against 147 us at R = 64)
+      if (more) stage(n0 + kTcCols);
+    }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-      if (!none) {
+      if (!none && 32 * warp < count) {
         uint32_t lo[16], hi[16];  // rows g, g + 8 and g + 16, g + 24
         const uint32_t at = tmem + (uint32_t(32 * warp) << 16) + 32 * h;
         tmem_ld_16x256b_x4(at, lo);
@@ -870,10 +888,11 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
           }
         }
       }
+      const int c = n0 + 32 * h + 8 * q;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (rows[k] >= 0 && c0 + 32 * h < a.C)
-          store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c0 + 32 * h, a.C, x[h][k]);
+        if (rows[k] >= 0 && c < a.C) store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c, a.C, x[h][k]);
+      if (more) fetch(n0 + kTcCols, h);
     }
   }
   __syncwarp();
@@ -1154,11 +1173,17 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
   const unsigned tiles = unsigned(max_tiles(M, L));
   if (R > 32 && M >= 64 * L) {
     const int halves = R > 64 ? 2 : 1, Rn = round16(int(R));
-    const int smem = halves * kTile * 128 + (GMN ? 2 * Rn * 128 : halves * kTcCols * 128) + kBarBytes + 1024;
+    const int gbytes = GMN ? 2 * Rn * 128 : halves * kTcCols * 128;
+    const int smem = halves * kTile * 128 + gbytes + kBarBytes + 1024;
     auto kern = expand_tc_kernel<BF16, GMN>;
     if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-    const ExpandTcArgs ta{a, err};
-    return launch_pdl(kern, dim3(unsigned((C + kTcCols - 1) / kTcCols), tiles), dim3(128), smem, st, ta) == cudaSuccess
+    // blocks of columns a block: up to four while there are three rounds of blocks
+    // ([8192, 16384], R = 128: 218, 193, 183 and 198 us with 1, 2, 4 and 8)
+    const int64_t blocks = (C + kTcCols - 1) / kTcCols, busy = (M + kTile - 1) / kTile;
+    int span = 1;
+    while (span < 4 && busy * (blocks / (2 * span)) >= 12 * sm_count()) span *= 2;
+    const ExpandTcArgs ta{a, span, err};
+    return launch_pdl(kern, dim3(unsigned((blocks + span - 1) / span), tiles), dim3(128), smem, st, ta) == cudaSuccess
                ? launch_status()
                : SPG_ERR_CUDA;
   }

@@ -290,13 +290,22 @@ __device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::
       v[k][i] = BETA ? f2_fma(z, g[i], b[i]) : f2_mul(z, g[i]);
     }
     if constexpr (S8) {
-      // clamp(rne(y qscale)); a NaN gives code 0
+      // clamp(rne(y qscale)): the conversion and the packing saturate at 127 and
+      // keep a NaN's 0; -128 is cut off before them by a maximum that passes NaN on
       uint32_t w[VE / 4];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float2 e = f2_get(v[k][i / 2]);
-        const int code = max(-127, min(127, __float2int_rn((i & 1 ? e.y : e.x) * a.qscale)));
-        w[i / 4] = (i % 4 ? w[i / 4] : 0u) | (static_cast<uint32_t>(code & 0xFF) << (8 * (i % 4)));
+      for (int i = 0; i < VE; i += 4) {
+        int code[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = f2_get(f2_mul(v[k][(i + e) / 2], f2_of(a.qscale, a.qscale)));
+          float f;
+          asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(e & 1 ? y.y : y.x), "f"(-127.f));
+          code[e] = __float2int_rn(f);
+        }
+        uint32_t hi;
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(code[3]), "r"(code[2]), "r"(0));
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w[i / 4]) : "r"(code[1]), "r"(code[0]), "r"(hi));
       }
       int8_t* o = static_cast<int8_t*>(a.y) + row * a.ldy + c;
       if (VECTORS && n >= VE) {
