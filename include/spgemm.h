@@ -408,7 +408,7 @@ spg_status spgemm_tw_f16_noalloc(const void* X, int64_t ldx, const spg_tw_desc* 
  *   Y    [M, C] of `dtype`, pitch ldy; Yq int8 [M, C], pitch ldy
  *   mean, rstd fp32 [M]: mu and r of each row for layernorm_bwd, or NULL
  * H and Y may be the same memory as X or res (same pointer and pitch), but not
- * as each other.  layernorm_bwd, with z = (h - mu) r and g = dY gamma:
+ * as each other; Yq is memory of its own.  layernorm_bwd, with z = (h - mu) r and g = dY gamma:
  *   dX = r (g - mean_c g - z mean_c(g z)) (+ dH), one rounding to `dtype`
  *   dgamma[c] = sum_m dY z,  dbeta[c] = sum_m dY, summed in fp32 in a fixed
  *   order, one rounding to wdtype

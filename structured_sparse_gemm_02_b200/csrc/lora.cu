@@ -7,14 +7,23 @@
 //
 // A plan (one small kernel per batch) groups the rows by adapter; every product
 // then runs on tiles of up to 128 rows of one adapter, whose rows TMA gathers
-// by index.  Three tcgen05 kernels cover all products:
-//   shrink  P = T G^T for T = X (G = A_l) or T = dY (G = B_l^T)
-//   expand  Y = base + s P G^T for G = B_l or G = A_l^T
-//   wgrad   dG = s T^T P for (X, U) and (dY, V)
+// by index.  Three kinds of kernels cover all products:
+//   shrink  P = T G^T for T = X (G = A_l) or T = dY (G = B_l^T): tcgen05
+//   expand  Y = base + s P G^T for G = B_l or G = A_l^T: mma.sync up to R = 32
+//           and for few rows, tcgen05 beyond
+//   wgrad   dG = s T^T P for (X, U) and (dY, V): tcgen05
+// The two that read dY run as one launch.
 // R is at most 128, so each of them is bound by the reads and writes of its
 // large matrix.  V and U are rounded to the activations' type between the
 // products: V is saved for the backward pass as any activation is, and both
 // are operands of the tensor cores; every sum is fp32.
+//
+// A block of a cluster may wait for tensor memory while another block of it
+// holds some, so such blocks of several streams must never use up an SM's tensor
+// memory between them: those of shrink, wgrad and dual take more than 520 bytes
+// of shared memory for each column (an SM has 456), and beside a block of the
+// pruned layers' kernels, which take nearly all of it, none fits.  Blocks of
+// the expand kernels wait for no other block.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -195,7 +204,6 @@ struct Ring {
   uint64_t* full;
   uint64_t* empty;
   uint64_t* done;
-  uint64_t* more;  // twelve further barriers (expand_kernel)
   uint32_t* tmem;
   volatile int* abort_flag;
 };
@@ -214,29 +222,25 @@ struct Turn {
   }
 };
 constexpr int kMaxStages = 8;
-constexpr int kBarBytes = (2 * kMaxStages + 13) * 8 + 16;
+constexpr int kBarBytes = (2 * kMaxStages + 1) * 8 + 8;
 
 __device__ __forceinline__ Ring ring_at(uint8_t* p) {
   Ring r;
   r.full = reinterpret_cast<uint64_t*>(p);
   r.empty = r.full + kMaxStages;
   r.done = r.empty + kMaxStages;
-  r.more = r.done + 1;
-  r.tmem = reinterpret_cast<uint32_t*>(r.more + 12);
+  r.tmem = reinterpret_cast<uint32_t*>(r.done + 1);
   r.abort_flag = reinterpret_cast<volatile int*>(r.tmem + 1);
   return r;
 }
 
-// `readers` arrivals free a stage; `more`: arrivals of the further barriers.
-__device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int warp, int readers = 1,
-                                          const int* more = nullptr) {
+__device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int warp) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&r.full[s], 1);
-      mbar_init(&r.empty[s], readers);
+      mbar_init(&r.empty[s], 1);
     }
     mbar_init(r.done, 1);
-    for (int i = 0; more && i < 12; ++i) mbar_init(&r.more[i], more[i]);
     *r.abort_flag = 0;
     fence_barrier_init();
   }
@@ -259,7 +263,7 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 
 __host__ __device__ inline int round16(int r) { return (r + 15) & ~15; }
 // Tensor-memory columns for n accumulator columns: a power of two, at least 32.
-__host__ __device__ inline uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : 256u; }
+__host__ __device__ inline uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : 128u; }
 
 // The 128-byte-swizzled tiles below are rows of 64 elements (128 bytes), eight
 // rows to a 1024-byte group.  Read with the row as the MMA's M or N index they
@@ -305,10 +309,10 @@ __device__ __forceinline__ TileRows tile_rows(const int* perm, int pos, int coun
   return t;
 }
 
-// Loads 64 columns from x of the tile's rows (32 groups of `rowb` bytes a row)
-// to dst.  exact: only the tile's rows may be read as anything but zeros, as
-// where the row is summed over.  Returns the bytes to expect, the same on
-// every lane; `issue` false only counts.
+// `rowb` bytes of each of the tile's rows, in `groups` groups of 32 rows, from
+// column x to dst.  EXACT: only the tile's rows may be read as anything but
+// zeros, as where the row is summed over.  rows_bytes: the bytes to expect, the
+// same on every lane.
 template <bool EXACT>
 __device__ __forceinline__ bool as_box(const TileRows& t, int g) {
   const int n = t.count - 32 * g;
@@ -823,7 +827,8 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
     } else {
       for (int i = threadIdx.x; i < kTcCols * pieces; i += 128) {
         const int v = i / pieces, c = i - v * pieces;  // column v of the block, piece c of its row
-        const int n = (v & ~31) + 8 * ((v >> 1) & 3) + 2 * ((v >> 3) & 3) + (v & 1);  // its place (the order is its own inverse)
+        // its place: the order is its own inverse
+        const int n = (v & ~31) + 8 * ((v >> 1) & 3) + 2 * ((v >> 3) & 3) + (v & 1);
         const bool ok = n0 + v < a.C && 8 * c < R;
         cp_async16(Gs + (c >> 3) * kTcCols * 128 + n * 128 + (((c & 7) ^ (n & 7)) << 4),
                    G + (ok ? int64_t(n0 + v) * R + 8 * c : 0), ok);
@@ -1205,7 +1210,8 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
                ? launch_status()
                : SPG_ERR_CUDA;
   };
-  return M >= 64 * L && busy > 0 && busy < 2 * sm_count() ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 1>());
+  return M >= 64 * L && busy > 0 && busy < 2 * sm_count() ? go(std::integral_constant<int, 4>())
+                                                          : go(std::integral_constant<int, 1>());
 }
 
 // Adapters that can have whole tiles of rows.
@@ -1323,8 +1329,9 @@ spg_status lora_plan(const int32_t* index, int64_t M, int64_t L, int32_t* plan, 
                      spg_stream_t stream) {
   using namespace spg;
   using namespace spg::lora;
-  if (M < 0 || L <= 0 || !plan || (M != 0 && !index)) return SPG_ERR_INVALID_ARG;
+  if (M < 0 || L <= 0) return SPG_ERR_INVALID_ARG;
   if (L > kMaxL || M >= (int64_t(1) << 22)) return SPG_ERR_UNSUPPORTED_SHAPE;
+  if (!plan || (M != 0 && !index)) return SPG_ERR_INVALID_ARG;
   if (plan_bytes < lora_plan_size(M, L)) return SPG_ERR_INVALID_ARG;
   if (!aligned(index, 4) || !aligned(plan, 16)) return SPG_ERR_MISALIGNED;
   spg_status rc = check_device();

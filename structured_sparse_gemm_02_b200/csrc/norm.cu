@@ -1030,6 +1030,11 @@ bool vec_ok(const void* p, int64_t ld, int es) { return p == nullptr || (aligned
 bool is_act(int d) { return d == SPG_F16 || d == SPG_BF16 || d == SPG_F32; }
 
 // What the two forward entry points share.
+// An output in place of an input keeps its rows where they are.
+bool other_pitch(const void* in, int64_t ldin, const void* out, int64_t ldout) {
+  return in && in == out && ldin != ldout;
+}
+
 spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void* H, int64_t ldh, const void* gamma,
                const void* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd, int64_t M, int64_t C,
                int dtype, int wdtype, int s8, float qscale, cudaStream_t st) {
@@ -1044,6 +1049,9 @@ spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void*
       !aligned(beta, wes) || !aligned(mean, 4) || !aligned(rstd, 4))
     return SPG_ERR_MISALIGNED;
   if (M == 0) return SPG_OK;
+  if (Y == H || other_pitch(X, ldx, H, ldh) || other_pitch(res, ldres, H, ldh) ||
+      (s8 ? Y == X || Y == res : other_pitch(X, ldx, Y, ldy) || other_pitch(res, ldres, Y, ldy)))
+    return SPG_ERR_INVALID_ARG;
   spg_status rc = check_device();
   if (rc != SPG_OK) return rc;
   const Shape s = fwd_shape(int(C), es);
@@ -1103,6 +1111,7 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
       !aligned(workspace, 16))
     return SPG_ERR_MISALIGNED;
   if (ws_bytes < layernorm_bwd_workspace_size(M, C, dtype)) return SPG_ERR_INVALID_ARG;
+  if (M != 0 && (other_pitch(dY, lddy, dX, lddx) || other_pitch(dH, lddh, dX, lddx))) return SPG_ERR_INVALID_ARG;
   spg_status rc = check_device();
   if (rc != SPG_OK) return rc;
   auto st = reinterpret_cast<cudaStream_t>(stream);

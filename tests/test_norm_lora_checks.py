@@ -95,6 +95,20 @@ def test_norm_argument_errors(f):
             assert f(qscale=q) == INVALID
 
 
+def test_norm_in_place_errors():
+    """In place means the same rows: another pitch, two outputs in one place or codes over their input are refused."""
+    two = dict(res=4096, ldres=64, H=8192, ldh=64)
+    assert _ln(ldy=72) == INVALID                                        # Y is X
+    assert _ln(Y=4096, **{**two, "ldres": 72}) == INVALID                # Y is res
+    assert _ln(Y=12288, **{**two, "H": 16, "ldh": 72}) == INVALID        # H is X
+    assert _ln(Y=12288, **{**two, "H": 4096, "ldh": 72}) == INVALID      # H is res
+    assert _ln(Y=8192, **two) == INVALID and _ln8(Y=8192, **two) == INVALID  # Y is H
+    assert _ln8() == INVALID and _ln8(Y=4096, **two) == INVALID          # codes over X, over res
+    assert _lnb(lddx=72) == INVALID                                      # dX is dY
+    assert _lnb(dY=4096, dH=16, lddh=72) == INVALID                      # dX is dH
+    assert _ln(M=0, ldy=72) == OK                                        # nothing is written
+
+
 def test_norm_workspace_size():
     size = spg.lib().layernorm_bwd_workspace_size
     assert size(0, 64, 0) == 0 and size(5, 0, 0) == 0 and size(5, 16385, 0) == 0 and size(5, 64, 2) == 0
@@ -152,6 +166,7 @@ def test_lora_plan_errors_and_sizes():
     assert L.lora_plan(None, 300, 5, 16, need, None) == INVALID and L.lora_plan(16, 300, 5, None, need, None) == INVALID
     assert L.lora_plan(16, 300, 5, 16, need - 1, None) == INVALID
     assert L.lora_plan(16, 300, 8193, 16, 1 << 30, None) == SHAPE
+    assert L.lora_plan(16, 1 << 22, 5, None, 0, None) == SHAPE  # as the binding calls it: no size, no plan
     assert L.lora_plan(18, 300, 5, 16, need, None) == MISALIGNED and L.lora_plan(16, 300, 5, 24, need, None) == MISALIGNED
     assert L.lora_bwd_workspace_size(300, 64, 64, 8, 5) >= 300 * 8 * 2 and L.lora_bwd_workspace_size(0, 64, 64, 8, 5) == 0
 
