@@ -534,9 +534,12 @@ constexpr int kRegCols = 64;  // columns of a warp
 template <int RG>
 struct RegShape {
   static constexpr int CG = RG == 1 ? 4 : 2;
-  static constexpr int THREADS = 32 * RG * CG;
+  static constexpr int WARPS = RG * CG;
+  static constexpr int THREADS = 32 * WARPS;
   static constexpr int COLS = CG * kRegCols;
   static constexpr int PITCH = COLS * 2 + 16;  // bytes of a staged row of G
+  static constexpr int STAGES = RG == 1 ? 2 : 1;
+  static constexpr int BASE = WARPS * (STAGES * 4096 + kTile * 4);
 };
 
 struct ExpandRegArgs {
@@ -546,87 +549,143 @@ struct ExpandRegArgs {
   const uint16_t* G;
   const uint16_t* base;  // nullptr: 0
   uint16_t* Y;
-  int64_t ldp, ldb, ldy;
+  uint32_t pitch_p, pitch_b, pitch_y;  // bytes
   int C, R;
 };
+// Row `row` of a matrix; with a 32-bit pitch that is one instruction.
+template <class T>
+__device__ __forceinline__ T* row_at(T* p, int row, uint32_t pitch) {
+  return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + uint64_t(uint32_t(row)) * pitch);
+}
 
 // The k index of an MMA step may be dealt to lanes in any order that both
 // operands share, and so may its n index: lane t of a quad takes 4 consecutive
 // k of a step (8 of a pair of steps), one load a row, and n-tile j of 32
 // columns holds columns 8 t + 2 j and the next, so that a lane ends up with 8
-// consecutive columns of a row: one 16-byte load of base and one store.
+// consecutive columns of a row: one 16-byte piece of base and one store.
+// What bounds the kernel is the number of bytes under way: each warp copies its
+// own columns of base to shared memory two groups of 32 rows ahead of the sums
+// ([8192, 16384], R = 16: 91 us, 5.9 TB/s; base read into registers a group ahead
+// 112 us; three groups ahead and as many blocks an SM as fit 98 us).
 //   KS: steps of 16 with G in registers (1 or 2); 0: any number, read per 32 rows
 template <bool BF16, bool GMN, int KS, int RG>
-__global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 1 ? 4 : 2) expand_reg_kernel(const ExpandRegArgs a) {
+__global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ? 4 : 3)
+    expand_reg_kernel(const ExpandRegArgs a) {
   using Sh = RegShape<RG>;
-  constexpr int kRegThreads = Sh::THREADS, kRegBlockCols = Sh::COLS, kRegPitch = Sh::PITCH;
-  extern __shared__ __align__(16) uint8_t gsm[];
+  constexpr int kStages = Sh::STAGES;
+  extern __shared__ __align__(128) uint8_t gsm[];
   const int warp = (threadIdx.x >> 5) % Sh::CG, lane = threadIdx.x & 31;
   const int first = 32 * ((threadIdx.x >> 5) / Sh::CG);  // this warp's first rows of the tile
   const int g = lane >> 2, q = lane & 3;
+  uint8_t* mine = gsm + (threadIdx.x >> 5) * kStages * 4096;
+  int* rowid = reinterpret_cast<int*>(gsm + Sh::WARPS * kStages * 4096) + (threadIdx.x >> 5) * kTile;
+  uint8_t* gst = gsm + Sh::BASE;
   griddep_launch_dependents();
   griddep_wait();
   const int4 t = a.plan.tiles[blockIdx.y];
   if (int(blockIdx.y) >= a.plan.hdr[0]) return;
   const int adapter = t.x, pos = t.y, count = t.z;
   if (adapter < 0 && a.base == a.Y) return;
-  const int nb = blockIdx.x * kRegBlockCols;
+  const int nb = blockIdx.x * Sh::COLS;
   const int n0 = nb + warp * kRegCols;
-  const int c0 = n0 + 8 * q;  // this lane's columns: c0 .. and c0 + 32 ..
+  const bool busy = n0 < a.C && first < count;
+  // rows of base, 128 bytes each; the halves of odd rows change places, so that
+  // eight lanes reading two rows' halves meet no bank twice
+  const bool full = n0 + kRegCols <= a.C;  // no column of this warp is past the end
+  auto copy = [&](int r0, int s) {
+    if (a.base && r0 < count) {
+      const int v = lane & 7, r1 = lane >> 3;
+      const int in = min(16, max(0, 2 * (a.C - (n0 + 8 * v))));  // bytes inside the row
+      const uint16_t* from = a.base + (in ? n0 + 8 * v : 0);
+      uint8_t* to = mine + s * 4096 + r1 * 128 + ((v ^ ((r1 & 1) << 2)) << 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool ok = r0 + 4 * i + r1 < count;
+        cp_async16(to + 512 * i, row_at(from, ok ? rowid[r0 + 4 * i + r1] : rowid[r0], a.pitch_b), ok ? in : 0);
+      }
+    }
+    cp_async_commit();
+  };
+  if (busy) {
+    for (int r = first + lane; r < count; r += 32) rowid[r] = a.plan.perm[pos + r];
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) copy(first + 32 * RG * s, s);
+  }
   // a group of 32 rows: g, g + 8, g + 16, g + 24 are this lane's
   auto find = [&](int r0, int (&rows)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = r0 + 8 * k + g;
-      rows[k] = r < count ? a.plan.perm[pos + r] : -1;
+      rows[k] = r < count ? rowid[r] : -1;
     }
   };
-  auto fetch = [&](const int (&rows)[4], int h, uint4 (&x)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.base && rows[k] >= 0 && c0 + 32 * h < a.C)
-        x[k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c0 + 32 * h, a.C);
-    }
+  auto piece = [&](int s, int h, int k) {
+    return a.base ? *reinterpret_cast<const uint4*>(mine + s * 4096 + (8 * k + g) * 128 +
+                                                    (((4 * h + q) ^ ((g & 1) << 2)) << 4))
+                  : make_uint4(0u, 0u, 0u, 0u);
   };
-  auto put = [&](const int (&rows)[4], int h, const uint4 (&x)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (rows[k] >= 0 && c0 + 32 * h < a.C)
-        store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c0 + 32 * h, a.C, x[k]);
+  auto put = [&](int row, int h, const uint4& v) {
+    uint16_t* to = row_at(a.Y + n0 + 8 * q, row, a.pitch_y);
+    const int c = n0 + 32 * h + 8 * q;
+    if (row < 0) return;
+    if (full) *reinterpret_cast<uint4*>(to + 32 * h) = v;
+    else if (c < a.C) store_cols8(to - (n0 + 8 * q), c, a.C, v);
   };
   int rows[4];
-  uint4 x[2][4];
-  find(first, rows);
-  fetch(rows, 0, x[0]);
-  fetch(rows, 1, x[1]);
   if (adapter < 0) {
-    for (int r0 = first; r0 < count; r0 += 32 * RG) {
-      int next[4];
-      find(r0 + 32 * RG, next);
+    if (!busy) return;
+    for (int r0 = first, s = 0; r0 < count; r0 += 32 * RG, s = s + 1 == kStages ? 0 : s + 1) {
+      find(r0, rows);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        put(rows, h, x[h]);
-        fetch(next, h, x[h]);
-      }
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) rows[k] = next[k];
+        for (int k = 0; k < 4; ++k) put(rows[k], h, piece(s, h, k));
+      __syncwarp();
+      copy(r0 + 32 * RG * kStages, s);
     }
     return;
   }
+  constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
+  // fragments of P: rows 16 m .. of the group, step pair kb
+  auto load_a = [&](const int (&rows)[4], int kb, int m, uint32_t (&f)[S][4]) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = rows[2 * m + r];
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (KS == 1) {
+        if (row >= 0 && 4 * q < a.R) {
+          const uint2 u = *reinterpret_cast<const uint2*>(row_at(a.P + 4 * q, row, a.pitch_p));
+          w.x = u.x;
+          w.y = u.y;
+        }
+        f[0][r] = w.x;
+        f[0][2 + r] = w.y;
+      } else {
+        const int k = kb * 32 + 8 * q;
+        if (row >= 0 && k < a.R) w = *reinterpret_cast<const uint4*>(row_at(a.P + 8 * q, row, a.pitch_p) + kb * 32);
+        f[0][r] = w.x;
+        f[0][2 + r] = w.y;
+        f[1][r] = w.z;
+        f[1][2 + r] = w.w;
+      }
+    }
+  };
   const float scale = a.scale ? a.scale[adapter] : 1.f;
   const uint16_t* G = a.G + int64_t(adapter) * a.C * a.R;
   if constexpr (GMN) {
     // G is [R][C]: its columns of this block to shared memory, rows and columns
     // in the order that the fragments take them; zeros past R and C
     const int krows = KS == 1 ? 16 : (a.R + 31) / 32 * 32;
-    for (int i = threadIdx.x; i < krows * (kRegBlockCols / 8); i += kRegThreads) {
-      const int k = i / (kRegBlockCols / 8), v = i % (kRegBlockCols / 8);
+    for (int i = threadIdx.x; i < krows * (Sh::COLS / 8); i += Sh::THREADS) {
+      const int k = i / (Sh::COLS / 8), v = i % (Sh::COLS / 8);
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (k < a.R && nb + 8 * v < a.C) w = *reinterpret_cast<const uint4*>(G + int64_t(k) * a.C + nb + 8 * v);
       const int kp = KS == 1 ? 8 * ((k >> 1) & 1) + 2 * (k >> 2) + (k & 1)
                              : (k & ~31) + 16 * ((k >> 2) & 1) + 8 * ((k >> 1) & 1) + 2 * ((k >> 3) & 3) + (k & 1);
-      uint32_t* to = reinterpret_cast<uint32_t*>(gsm + kp * kRegPitch + (v >> 2) * 64 + (v & 3) * 4);
+      uint32_t* to = reinterpret_cast<uint32_t*>(gst + kp * Sh::PITCH + (v >> 2) * 64 + (v & 3) * 4);
       to[0] = w.x;
       to[4] = w.y;
       to[8] = w.z;
@@ -634,16 +693,16 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 1 ? 4 : 2) expand
     }
     __syncthreads();
   }
-  if (n0 >= a.C || first >= count) return;
+  if (!busy) return;
   // fragments of G for step pair kb (KS == 1: the one step) and half h: b[j][step][2]
-  auto load_b = [&](int kb, int h, uint32_t (&b)[4][KS == 1 ? 1 : 2][2]) {
+  auto load_b = [&](int kb, int h, uint32_t (&b)[4][S][2]) {
     if constexpr (GMN) {
 #pragma unroll
-      for (int s = 0; s < (KS == 1 ? 1 : 2); ++s)
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           // matrices: k rows 0-7 and 8-15 of tile j, then of tile j + 1
-          const uint32_t at = smem_addr(gsm + (kb * 32 + s * 16 + (lane & 15)) * kRegPitch +
+          const uint32_t at = smem_addr(gst + (kb * 32 + s * 16 + (lane & 15)) * Sh::PITCH +
                                         (warp * kRegCols + 32 * h) * 2 + (j + (lane >> 4)) * 16);
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                        : "=r"(b[j][s][0]), "=r"(b[j][s][1]), "=r"(b[j + 1][s][0]), "=r"(b[j + 1][s][1])
@@ -670,84 +729,61 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 1 ? 4 : 2) expand
       }
     }
   };
-  auto load_a = [&](const int (&rows)[4], int kb, uint32_t (&f)[2][KS == 1 ? 1 : 2][4]) {
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = rows[2 * m + r];
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (KS == 1) {
-          if (row >= 0 && 4 * q < a.R) {
-            const uint2 u = *reinterpret_cast<const uint2*>(a.P + int64_t(row) * a.ldp + 4 * q);
-            w.x = u.x;
-            w.y = u.y;
-          }
-          f[m][0][r] = w.x;
-          f[m][0][2 + r] = w.y;
-        } else {
-          const int k = kb * 32 + 8 * q;
-          if (row >= 0 && k < a.R) w = *reinterpret_cast<const uint4*>(a.P + int64_t(row) * a.ldp + k);
-          f[m][0][r] = w.x;
-          f[m][0][2 + r] = w.y;
-          f[m][1][r] = w.z;
-          f[m][1][2 + r] = w.w;
-        }
-      }
-  };
-  constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
-  uint32_t held[KS ? 2 : 1][4][S][2];
+  uint32_t held[KS ? 2 : 1][4][S][2], f[2][S][4];
+  find(first, rows);
   if constexpr (KS > 0) {
     load_b(0, 0, held[0]);
     load_b(0, 1, held[1]);
+    load_a(rows, 0, 0, f[0]);
+    load_a(rows, 0, 1, f[1]);
   }
-  // The next group's rows of P and base are read as soon as their registers
-  // are free, half by half: with all reads at the head of a group the kernel
-  // waited for them (16 warps an SM) and took 103 us for [8192, 16384].
-  uint32_t f[2][S][4];
-  if constexpr (KS > 0) load_a(rows, 0, f);
-  for (int r0 = first; r0 < count; r0 += 32 * RG) {
+  for (int r0 = first, s = 0; r0 < count; r0 += 32 * RG, s = s + 1 == kStages ? 0 : s + 1) {
     int next[4];
     find(r0 + 32 * RG, next);
-    const int pairs = KS ? 1 : (a.R + 31) / 32;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float acc[2][4][4];  // [m tile][n tile]
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m) {
+        float acc[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-      for (int kb = 0; kb < pairs; ++kb) {
-        if constexpr (KS == 0) {
-          load_a(rows, kb, f);
-          load_b(kb, h, held[0]);
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+        auto product = [&](const uint32_t(&fa)[S][4], const uint32_t(&b)[4][S][2]) {
+#pragma unroll
+          for (int st = 0; st < S; ++st)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16816<BF16>(acc[j], fa[st], b[j][st][0], b[j][st][1]);
+        };
+        if constexpr (KS > 0) {
+          product(f[m], held[h]);
+          if (h == 1) load_a(next, 0, m, f[m]);  // the next group's, as soon as the registers are free
+        } else {
+          for (int kb = 0; kb < (a.R + 31) / 32; ++kb) {
+            load_a(rows, kb, m, f[0]);
+            load_b(kb, h, held[0]);
+            product(f[0], held[0]);
+          }
         }
-        const auto& b = held[KS ? h : 0];
+        if (h == 0 && m == 0) {
+          cp_async_wait<kStages - 1>();
+          __syncwarp();
+        }
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int r = 0; r < 2; ++r) {
+          uint4 x = piece(s, h, 2 * m + r);
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816<BF16>(acc[m][j], f[m][s], b[j][s][0], b[j][s][1]);
-      }
-      if constexpr (KS > 0) {
-        if (h == 1) load_a(next, 0, f);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float(&d)[4][4] = acc[k >> 1];
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x[h][k]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 b = unpack2<BF16>(w[j]);
-          w[j] = pack2<BF16>(fmaf(scale, d[j][2 * (k & 1)], b.x), fmaf(scale, d[j][2 * (k & 1) + 1], b.y));
+          for (int j = 0; j < 4; ++j) {
+            const float2 b = unpack2<BF16>(w[j]);
+            w[j] = pack2<BF16>(fmaf(scale, acc[j][2 * r], b.x), fmaf(scale, acc[j][2 * r + 1], b.y));
+          }
+          put(rows[2 * m + r], h, x);
         }
       }
-      put(rows, h, x[h]);
-      fetch(next, h, x[h]);
     }
+    __syncwarp();
+    copy(r0 + 32 * RG * kStages, s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) rows[k] = next[k];
   }
@@ -775,11 +811,10 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
   uint8_t* smem = align1024(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
-  const int R = a.R, Rn = round16(R), halves = R > 64 ? 2 : 1;
-  const int gbytes = GMN ? 2 * Rn * 128 : halves * kTcCols * 128;
-  uint8_t* Ps = smem;                       // [128 rows][R], K-major
-  uint8_t* Gs = Ps + halves * kTile * 128;  // [128 columns][R], K-major, or [R][2 x 64 columns], N-major
-  const Ring ring = ring_at(Gs + gbytes);
+  const int R = a.R, Rn = round16(R), chunks = (Rn + 63) / 64;
+  uint8_t* Ps = smem;               // [128 rows][64 of R], K-major
+  uint8_t* Gs = Ps + kTile * 128;   // [128 columns][64 of R], K-major, or [64 of R][2 x 64 columns], N-major
+  const Ring ring = ring_at(Gs + kTcCols * 128);
   ring_init(ring, kTcCols, warp);
   const uint32_t tmem = *ring.tmem;
   griddep_wait();
@@ -804,7 +839,7 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       x[h][k] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.base && rows[k] >= 0 && c < last) x[h][k] = load_cols8(a.base + int64_t(rows[k]) * a.ldb, c, a.C);
+      if (a.base && rows[k] >= 0 && c < last) x[h][k] = load_cols8(row_at(a.base, rows[k], a.pitch_b), c, a.C);
     }
   };
 #pragma unroll
@@ -812,55 +847,58 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
   // Operands in 128-byte swizzled rows of 64: piece c of row r sits at c ^ (r % 8).
   // All copies are under way before any is waited for: with loads and stores
   // through registers R = 64 took 182 us.
-  const int pieces = Rn / 8;
   const uint16_t* G = a.G + int64_t(none ? 0 : adapter) * a.C * R;
-  auto stage = [&](int n0) {
+  auto stage_p = [&](int kc) {
+    const int pieces = min(64, Rn - 64 * kc) / 8;
+    for (int i = threadIdx.x; i < count * pieces; i += 128) {
+      const int r = i / pieces, c = i - r * pieces, k = 64 * kc + 8 * c;
+      const bool ok = k < R;
+      cp_async16(Ps + r * 128 + ((c ^ (r & 7)) << 4), row_at(a.P + (ok ? k : 0), a.plan.perm[pos + r], a.pitch_p),
+                 ok ? 16 : 0);
+    }
+  };
+  auto stage_g = [&](int n0, int kc) {
     // column 32 i + 8 j + 2 k + e of the MMA is column 32 i + 8 k + 2 j + e of G
+    const int depth = min(64, Rn - 64 * kc);
     if constexpr (GMN) {
-      for (int i = threadIdx.x; i < Rn * (kTcCols / 2); i += 128) {  // pairs of columns
+      for (int i = threadIdx.x; i < depth * (kTcCols / 2); i += 128) {  // pairs of columns
         const int k = i / (kTcCols / 2), v = i % (kTcCols / 2);
         const int c = 4 * ((v >> 4) & 1) + (v & 3);  // piece of the 64 columns, and 4 bytes of it
-        const bool ok = k < R && n0 + 2 * v < a.C;
-        cp_async4(Gs + (v >> 5) * Rn * 128 + k * 128 + ((c ^ (k & 7)) << 4) + ((v >> 2) & 3) * 4,
-                  G + (ok ? int64_t(k) * a.C + n0 + 2 * v : 0), ok);
+        const bool ok = 64 * kc + k < R && n0 + 2 * v < a.C;
+        cp_async4(Gs + (v >> 5) * 64 * 128 + k * 128 + ((c ^ (k & 7)) << 4) + ((v >> 2) & 3) * 4,
+                  G + (ok ? int64_t(64 * kc + k) * a.C + n0 + 2 * v : 0), ok);
       }
     } else {
+      const int pieces = depth / 8;
       for (int i = threadIdx.x; i < kTcCols * pieces; i += 128) {
-        const int v = i / pieces, c = i - v * pieces;  // column v of the block, piece c of its row
+        const int v = i / pieces, c = i - v * pieces, k = 64 * kc + 8 * c;  // column v of the block, k .. of its row
         // its place: the order is its own inverse
         const int n = (v & ~31) + 8 * ((v >> 1) & 3) + 2 * ((v >> 3) & 3) + (v & 1);
-        const bool ok = n0 + v < a.C && 8 * c < R;
-        cp_async16(Gs + (c >> 3) * kTcCols * 128 + n * 128 + (((c & 7) ^ (n & 7)) << 4),
-                   G + (ok ? int64_t(n0 + v) * R + 8 * c : 0), ok);
+        const bool ok = n0 + v < a.C && k < R;
+        cp_async16(Gs + n * 128 + ((c ^ (n & 7)) << 4), G + (ok ? int64_t(n0 + v) * R + k : 0), ok ? 16 : 0);
       }
     }
   };
   if (!none) {
-    for (int i = threadIdx.x; i < count * pieces; i += 128) {
-      const int r = i / pieces, c = i - r * pieces;
-      const bool ok = 8 * c < R;
-      cp_async16(Ps + (c >> 3) * kTile * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                 a.P + int64_t(a.plan.perm[pos + r]) * a.ldp + (ok ? 8 * c : 0), ok);
-    }
-    stage(first);
+    stage_p(0);
+    stage_g(first, 0);
   }
   const float scale = none ? 0.f : a.scale ? a.scale[adapter] : 1.f;
   const uint32_t idesc = instr_desc_major(BF16, kTile, kTcCols, 0, GMN ? 1 : 0);
   uint32_t phase = 0;
   for (int n0 = first; n0 < last; n0 += kTcCols) {
     const bool more = n0 + kTcCols < last;
-    if (!none) {
+    for (int kc = 0; kc < chunks && !none; ++kc) {
       cp_async_wait_all();
       fence_proxy_async_smem();
       tc_fence_before();
       __syncthreads();  // operands are there, and the accumulators of the last columns have been read
       tc_fence_after();
       if (threadIdx.x == 0) {
-        for (int k = 0; k < Rn / 16; ++k) {
-          const uint64_t ad = desc_k_major(Ps + (k >> 2) * kTile * 128) + ((32 * (k & 3)) >> 4);
-          const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, Rn * 128)
-                                  : desc_k_major(Gs + (k >> 2) * kTcCols * 128) + ((32 * (k & 3)) >> 4);
-          tc_mma(tmem, ad, bd, idesc, k != 0);
+        for (int k = 0; k < min(64, Rn - 64 * kc) / 16; ++k) {
+          const uint64_t ad = desc_k_major(Ps) + ((32 * k) >> 4);
+          const uint64_t bd = GMN ? desc_mn_major(Gs + 2048 * k, 64 * 128) : desc_k_major(Gs) + ((32 * k) >> 4);
+          tc_mma(tmem, ad, bd, idesc, (kc | k) != 0);
         }
         tc_commit(ring.done);
       }
@@ -869,9 +907,13 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
       phase ^= 1u;
       __syncwarp();
       tc_fence_after();
-      // the product has read G: the next one is copied behind the sums (a second
-      // buffer costs a block an SM: 159 against 147 us at R = 64)
-      if (more) stage(n0 + kTcCols);
+      // the product has read its operands: the next ones are copied, the last
+      // time behind the sums (a second buffer of G: 159 against 147 us at R = 64)
+      const bool last_chunk = kc + 1 == chunks;
+      if (!last_chunk || more) {
+        if (chunks > 1) stage_p(last_chunk ? 0 : kc + 1);
+        last_chunk ? stage_g(n0 + kTcCols, 0) : stage_g(n0, kc + 1);
+      }
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -896,7 +938,7 @@ __global__ void __launch_bounds__(128, 4) expand_tc_kernel(const ExpandTcArgs ta
       const int c = n0 + 32 * h + 8 * q;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (rows[k] >= 0 && c < a.C) store_cols8(a.Y + int64_t(rows[k]) * a.ldy, c, a.C, x[h][k]);
+        if (rows[k] >= 0 && c < a.C) store_cols8(row_at(a.Y, rows[k], a.pitch_y), c, a.C, x[h][k]);
       if (more) fetch(n0 + kTcCols, h);
     }
   }
@@ -1174,12 +1216,11 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
                   int64_t ldb, void* Y, int64_t ldy, int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err,
                   cudaStream_t st) {
   const ExpandRegArgs a{plan, scale, static_cast<const uint16_t*>(P), static_cast<const uint16_t*>(G),
-                        static_cast<const uint16_t*>(base), static_cast<uint16_t*>(Y), ldp, ldb, ldy, int(C), int(R)};
+                        static_cast<const uint16_t*>(base), static_cast<uint16_t*>(Y), uint32_t(ldp * 2), uint32_t(ldb * 2),
+                        uint32_t(ldy * 2), int(C), int(R)};
   const unsigned tiles = unsigned(max_tiles(M, L));
   if (R > 32 && M >= 64 * L) {
-    const int halves = R > 64 ? 2 : 1, Rn = round16(int(R));
-    const int gbytes = GMN ? 2 * Rn * 128 : halves * kTcCols * 128;
-    const int smem = halves * kTile * 128 + gbytes + kBarBytes + 1024;
+    const int smem = (kTile + kTcCols) * 128 + kBarBytes + 1024;
     auto kern = expand_tc_kernel<BF16, GMN>;
     if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
     // blocks of columns a block: up to four while there are three rounds of blocks
@@ -1187,10 +1228,12 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
     const int64_t blocks = (C + kTcCols - 1) / kTcCols, busy = (M + kTile - 1) / kTile;
     int span = 1;
     while (span < 4 && busy * (blocks / (2 * span)) >= 12 * sm_count()) span *= 2;
+    // Not launched ahead of the shrink's end: an SM that never idles keeps the
+    // shrink's large share of shared memory, and the loads of base under way are
+    // limited by what that leaves to L1 (R = 64: 144 against 119 us).
     const ExpandTcArgs ta{a, span, err};
-    return launch_pdl(kern, dim3(unsigned((blocks + span - 1) / span), tiles), dim3(128), smem, st, ta) == cudaSuccess
-               ? launch_status()
-               : SPG_ERR_CUDA;
+    kern<<<dim3(unsigned((blocks + span - 1) / span), tiles), dim3(128), smem, st>>>(ta);
+    return launch_status();
   }
   // Few whole tiles: their groups of 32 rows go to warps side by side (M 1024,
   // C 4096: 16.0 against 17.4 us with a group after the other); otherwise a warp
@@ -1203,8 +1246,8 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
     auto kern = R <= 16   ? expand_reg_kernel<BF16, GMN, 1, RG>
                 : R <= 32 ? expand_reg_kernel<BF16, GMN, 2, RG>
                           : expand_reg_kernel<BF16, GMN, 0, RG>;
-    const int smem = GMN ? (R <= 16 ? 16 : (int(R) + 31) / 32 * 32) * Sh::PITCH : 0;
-    if (smem > 48 * 1024 && prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
+    const int smem = Sh::BASE + (GMN ? (R <= 16 ? 16 : (int(R) + 31) / 32 * 32) * Sh::PITCH : 0);
+    if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
     return launch_pdl(kern, dim3(unsigned((C + Sh::COLS - 1) / Sh::COLS), tiles), dim3(Sh::THREADS), smem, st, a) ==
                    cudaSuccess
                ? launch_status()
