@@ -791,12 +791,13 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
 
 // ---- expand for larger R: the same with tcgen05 ------------------------------------------
 // A block takes a tile and `span` blocks of 128 columns.  The product comes from
-// one MMA chain over R (with mma.sync the operands' traffic through L1 grows
-// with R: 198 us for [8192, 16384] at R = 64, 300 us at R = 128); base is in
-// registers before it and is added in the same layout, which tcgen05.ld
+// MMAs over R in chunks of 64 (with mma.sync the operands' traffic through L1
+// grows with R: 142 us for [8192, 16384] at R = 64, 273 us at R = 128; now 117
+// and 165; R in one piece leaves room for three blocks an SM: 172 us).  base is
+// in registers before it and is added in the same layout, which tcgen05.ld
 // 16x256b and a permuted order of G's columns in shared memory give: a lane has
-// 8 consecutive columns of a row.  P is staged once a block; base of the next
-// columns is read as the registers of this one's become free.
+// 8 consecutive columns of a row.  Up to R = 64 P is staged once a block; base of
+// the next columns is read as the registers of this one's become free.
 struct ExpandTcArgs {
   ExpandRegArgs a;
   int span;
@@ -1223,11 +1224,10 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
     const int smem = (kTile + kTcCols) * 128 + kBarBytes + 1024;
     auto kern = expand_tc_kernel<BF16, GMN>;
     if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-    // blocks of columns a block: up to four while there are three rounds of blocks
-    // ([8192, 16384], R = 128: 218, 193, 183 and 198 us with 1, 2, 4 and 8)
+    // two blocks of columns a block while there are three rounds of blocks
+    // ([8192, 16384], R = 64: 126, 117 and 119 us with 1, 2 and 4; [1024, 4096]: 15, 19 and 26)
     const int64_t blocks = (C + kTcCols - 1) / kTcCols, busy = (M + kTile - 1) / kTile;
-    int span = 1;
-    while (span < 4 && busy * (blocks / (2 * span)) >= 12 * sm_count()) span *= 2;
+    const int span = busy * (blocks / 2) >= 12 * sm_count() ? 2 : 1;
     // Not launched ahead of the shrink's end: an SM that never idles keeps the
     // shrink's large share of shared memory, and the loads of base under way are
     // limited by what that leaves to L1 (R = 64: 144 against 119 us).
