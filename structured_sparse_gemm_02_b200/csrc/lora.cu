@@ -606,8 +606,56 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     }
     cp_async_commit();
   };
+  constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
+  const uint16_t* G = a.G + int64_t(adapter < 0 ? 0 : adapter) * a.C * a.R;
+  // fragments of G for step pair kb (KS == 1: the one step) and half h: b[j][step][2]
+  auto load_b = [&](int kb, int h, uint32_t (&b)[4][S][2]) {
+    if constexpr (GMN) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          // matrices: k rows 0-7 and 8-15 of tile j, then of tile j + 1
+          const uint32_t at = smem_addr(gst + (kb * 32 + s * 16 + (lane & 15)) * Sh::PITCH +
+                                        (warp * kRegCols + 32 * h) * 2 + (j + (lane >> 4)) * 16);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(b[j][s][0]), "=r"(b[j][s][1]), "=r"(b[j + 1][s][0]), "=r"(b[j + 1][s][1])
+                       : "r"(at));
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        int n = n0 + 32 * h + 8 * (g >> 1) + 2 * j + (g & 1);
+        n = n < a.C ? n : a.C - 1;  // a column past the end is not stored
+        const uint16_t* from = G + int64_t(n) * a.R;
+        if constexpr (KS == 1) {
+          const uint2 w = 4 * q < a.R ? *reinterpret_cast<const uint2*>(from + 4 * q) : make_uint2(0u, 0u);
+          b[j][0][0] = w.x;
+          b[j][0][1] = w.y;
+        } else {
+          const int k = kb * 32 + 8 * q;
+          const uint4 w = k < a.R ? *reinterpret_cast<const uint4*>(from + k) : make_uint4(0u, 0u, 0u, 0u);
+          b[j][0][0] = w.x;
+          b[j][0][1] = w.y;
+          b[j][1][0] = w.z;
+          b[j][1][1] = w.w;
+        }
+      }
+    }
+  };
+  uint32_t held[KS ? 2 : 1][4][S][2], f[2][S][4];
   if (busy) {
-    for (int r = first + lane; r < count; r += 32) rowid[r] = a.plan.perm[pos + r];
+    int found[kTile / 32];
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i)
+      found[i] = first + 32 * i + lane < count ? a.plan.perm[pos + first + 32 * i + lane] : 0;
+    if constexpr (KS > 0 && !GMN) {  // G does not wait for the rows
+      load_b(0, 0, held[0]);
+      load_b(0, 1, held[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i)
+      if (first + 32 * i + lane < count) rowid[first + 32 * i + lane] = found[i];
     __syncwarp();
 #pragma unroll
     for (int s = 0; s < kStages; ++s) copy(first + 32 * RG * s, s);
@@ -648,7 +696,6 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     }
     return;
   }
-  constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
   // fragments of P: rows 16 m .. of the group, step pair kb
   auto load_a = [&](const int (&rows)[4], int kb, int m, uint32_t (&f)[S][4]) {
 #pragma unroll
@@ -674,7 +721,6 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     }
   };
   const float scale = a.scale ? a.scale[adapter] : 1.f;
-  const uint16_t* G = a.G + int64_t(adapter) * a.C * a.R;
   if constexpr (GMN) {
     // G is [R][C]: its columns of this block to shared memory, rows and columns
     // in the order that the fragments take them; zeros past R and C
@@ -694,46 +740,12 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     __syncthreads();
   }
   if (!busy) return;
-  // fragments of G for step pair kb (KS == 1: the one step) and half h: b[j][step][2]
-  auto load_b = [&](int kb, int h, uint32_t (&b)[4][S][2]) {
-    if constexpr (GMN) {
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          // matrices: k rows 0-7 and 8-15 of tile j, then of tile j + 1
-          const uint32_t at = smem_addr(gst + (kb * 32 + s * 16 + (lane & 15)) * Sh::PITCH +
-                                        (warp * kRegCols + 32 * h) * 2 + (j + (lane >> 4)) * 16);
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(b[j][s][0]), "=r"(b[j][s][1]), "=r"(b[j + 1][s][0]), "=r"(b[j + 1][s][1])
-                       : "r"(at));
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int n = n0 + 32 * h + 8 * (g >> 1) + 2 * j + (g & 1);
-        n = n < a.C ? n : a.C - 1;  // a column past the end is not stored
-        const uint16_t* from = G + int64_t(n) * a.R;
-        if constexpr (KS == 1) {
-          const uint2 w = 4 * q < a.R ? *reinterpret_cast<const uint2*>(from + 4 * q) : make_uint2(0u, 0u);
-          b[j][0][0] = w.x;
-          b[j][0][1] = w.y;
-        } else {
-          const int k = kb * 32 + 8 * q;
-          const uint4 w = k < a.R ? *reinterpret_cast<const uint4*>(from + k) : make_uint4(0u, 0u, 0u, 0u);
-          b[j][0][0] = w.x;
-          b[j][0][1] = w.y;
-          b[j][1][0] = w.z;
-          b[j][1][1] = w.w;
-        }
-      }
-    }
-  };
-  uint32_t held[KS ? 2 : 1][4][S][2], f[2][S][4];
   find(first, rows);
   if constexpr (KS > 0) {
-    load_b(0, 0, held[0]);
-    load_b(0, 1, held[1]);
+    if constexpr (GMN) {
+      load_b(0, 0, held[0]);
+      load_b(0, 1, held[1]);
+    }
     load_a(rows, 0, 0, f[0]);
     load_a(rows, 0, 1, f[1]);
   }
