@@ -42,6 +42,7 @@ namespace lora {
 constexpr int kTile = 128;  // rows of a tile: the M of one MMA
 constexpr int kMaxL = 8192;
 constexpr int kMaxR = 128;
+constexpr int64_t kMaxPitch = int64_t(1) << 31;  // pitches in bytes fit 32 bits
 
 // ---- the plan ---------------------------------------------------------------------
 // int32 words: [0] number of tiles; start[L + 2] (rows of each adapter, then
@@ -363,9 +364,14 @@ struct ShrinkArgs {
   const float* scale;  // nullptr: 1
   void* P;
   int64_t ldp;
-  int M, D, R, stages, gbytes, rowb;
+  int M, D, R, stages, trows, gbytes, rowb;
   uint32_t* err;
 };
+
+// Bytes of a shrink's ring: its last stage is read as a whole tile.
+__host__ __device__ inline int ring_of(int stages, int stage) {
+  return stages * stage + (stage < kTile * 128 ? kTile * 128 - stage : 0);
+}
 
 template <bool BF16, bool GMN>
 __device__ __forceinline__ void shrink_body(uint8_t* smem, const CUtensorMap& tmT, const CUtensorMap& tmT1,
@@ -374,8 +380,10 @@ __device__ __forceinline__ void shrink_body(uint8_t* smem, const CUtensorMap& tm
   const int cs = cluster_nctarank(), rank = cluster_ctarank();
   const int R = a.R, vecs = R / 8;
   const int Rn = round16(R);
-  const int stage_bytes = kTile * 128 + a.gbytes;
-  const int ring_bytes = a.stages * stage_bytes, part_bytes = kTile * (R + 4) * 4;
+  // A tile has at most a.trows rows (M, where that is less than a whole tile); the
+  // MMA reads 128, the others from whatever follows, and nobody reads their sums
+  const int tbytes = a.trows * 128, stage_bytes = tbytes + a.gbytes;
+  const int ring_bytes = ring_of(a.stages, stage_bytes), part_bytes = kTile * (R + 4) * 4;
   const Ring ring = ring_at(smem + (ring_bytes > part_bytes ? ring_bytes : part_bytes));
   ring_init(ring, tmem_cols(Rn), warp);
   const uint32_t tmem = *ring.tmem;
@@ -408,10 +416,10 @@ __device__ __forceinline__ void shrink_body(uint8_t* smem, const CUtensorMap& tm
       rows_load<false>(rows, 4, 128, st, &tmT, &tmT1, k, &ring.full[s], lane);
       if (lane == 0) {
         if constexpr (GMN) {
-          tma_load_3d(st + kTile * 128, &tmG, 0, k, adapter, &ring.full[s]);
-          if (R > 64) tma_load_3d(st + kTile * 128 + 8192, &tmG, 64, k, adapter, &ring.full[s]);
+          tma_load_3d(st + tbytes, &tmG, 0, k, adapter, &ring.full[s]);
+          if (R > 64) tma_load_3d(st + tbytes + 8192, &tmG, 64, k, adapter, &ring.full[s]);
         } else {
-          tma_load_3d(st + kTile * 128, &tmG, k, 0, adapter, &ring.full[s]);
+          tma_load_3d(st + tbytes, &tmG, k, 0, adapter, &ring.full[s]);
         }
       }
       __syncwarp();
@@ -423,7 +431,7 @@ __device__ __forceinline__ void shrink_body(uint8_t* smem, const CUtensorMap& tm
     if (lane == 0) {
       const uint32_t idesc = instr_desc_major(BF16, kTile, Rn, 0, GMN ? 1 : 0);
       const uint64_t ad0 = desc_k_major(smem);
-      const uint64_t bd0 = GMN ? desc_rows(smem + kTile * 128, a.rowb, 8192) : desc_k_major(smem + kTile * 128);
+      const uint64_t bd0 = GMN ? desc_rows(smem + tbytes, a.rowb, 8192) : desc_k_major(smem + tbytes);
       const int bstep = (GMN ? 16 * a.rowb : 32) >> 4;
       Turn r(a.stages);
       for (int i = 0; i < n; ++i, r.next()) {
@@ -567,8 +575,10 @@ __device__ __forceinline__ T* row_at(T* p, int row, uint32_t pitch) {
 // own columns of base to shared memory two groups of 32 rows ahead of the sums
 // ([8192, 16384], R = 16: 91 us, 5.9 TB/s; base read into registers a group ahead
 // 112 us; three groups ahead and as many blocks an SM as fit 98 us).
+// Where adapters have few rows, what is read is mostly G: a warp then walks along
+// the columns (WALK), and reads G and base of the next ones behind the sums.
 //   KS: steps of 16 with G in registers (1 or 2); 0: any number, read per 32 rows
-template <bool BF16, bool GMN, int KS, int RG>
+template <bool BF16, bool GMN, int KS, int RG, bool WALK>
 __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ? 4 : 3)
     expand_reg_kernel(const ExpandRegArgs a) {
   using Sh = RegShape<RG>;
@@ -587,29 +597,42 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
   const int adapter = t.x, pos = t.y, count = t.z;
   if (adapter < 0 && a.base == a.Y) return;
   const int nb = blockIdx.x * Sh::COLS;
-  const int n0 = nb + warp * kRegCols;
+  int n0 = nb + warp * kRegCols;
   const bool busy = n0 < a.C && first < count;
+  // from a group of 32 rows to the next, and to the next columns behind the last
+  auto advance = [&](int& n, int& r0) {
+    r0 += 32 * RG;
+    if constexpr (WALK) {
+      if (r0 >= count) {
+        const int stride = gridDim.x * Sh::COLS;
+        r0 = first;
+        n = a.C - n > stride ? n + stride : a.C;
+      }
+    }
+  };
   // rows of base, 128 bytes each; the halves of odd rows change places, so that
   // eight lanes reading two rows' halves meet no bank twice
-  const bool full = n0 + kRegCols <= a.C;  // no column of this warp is past the end
-  auto copy = [&](int r0, int s) {
-    if (a.base && r0 < count) {
-      const int v = lane & 7, r1 = lane >> 3;
-      const int in = min(16, max(0, 2 * (a.C - (n0 + 8 * v))));  // bytes inside the row
-      const uint16_t* from = a.base + (in ? n0 + 8 * v : 0);
+  int nf = n0, rf = first;  // what is copied next
+  auto copy = [&](int s) {
+    if (a.base && rf < count && nf < a.C) {
+      const int v = lane & 7, r1 = lane >> 3, r0 = rf;
+      const int in = 2 * min(8, max(0, a.C - (nf + 8 * v)));  // bytes inside the row
+      const uint16_t* from = a.base + (in ? nf + 8 * v : 0);
       uint8_t* to = mine + s * 4096 + r1 * 128 + ((v ^ ((r1 & 1) << 2)) << 4);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        if (WALK && r0 + 4 * i >= count) break;
         const bool ok = r0 + 4 * i + r1 < count;
         cp_async16(to + 512 * i, row_at(from, ok ? rowid[r0 + 4 * i + r1] : rowid[r0], a.pitch_b), ok ? in : 0);
       }
     }
     cp_async_commit();
+    advance(nf, rf);
   };
   constexpr int S = KS == 1 ? 1 : 2;  // steps of a fragment
   const uint16_t* G = a.G + int64_t(adapter < 0 ? 0 : adapter) * a.C * a.R;
   // fragments of G for step pair kb (KS == 1: the one step) and half h: b[j][step][2]
-  auto load_b = [&](int kb, int h, uint32_t (&b)[4][S][2]) {
+  auto load_b = [&](int c, int kb, int h, uint32_t (&b)[4][S][2]) {  // columns from c
     if constexpr (GMN) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
@@ -625,7 +648,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        int n = n0 + 32 * h + 8 * (g >> 1) + 2 * j + (g & 1);
+        int n = c + 32 * h + 8 * (g >> 1) + 2 * j + (g & 1);
         n = n < a.C ? n : a.C - 1;  // a column past the end is not stored
         const uint16_t* from = G + int64_t(n) * a.R;
         if constexpr (KS == 1) {
@@ -650,15 +673,15 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     for (int i = 0; i < kTile / 32; ++i)
       found[i] = first + 32 * i + lane < count ? a.plan.perm[pos + first + 32 * i + lane] : 0;
     if constexpr (KS > 0 && !GMN) {  // G does not wait for the rows
-      load_b(0, 0, held[0]);
-      load_b(0, 1, held[1]);
+      load_b(n0, 0, 0, held[0]);
+      load_b(n0, 0, 1, held[1]);
     }
 #pragma unroll
     for (int i = 0; i < kTile / 32; ++i)
       if (first + 32 * i + lane < count) rowid[first + 32 * i + lane] = found[i];
     __syncwarp();
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) copy(first + 32 * RG * s, s);
+    for (int s = 0; s < kStages; ++s) copy(s);
   }
   // a group of 32 rows: g, g + 8, g + 16, g + 24 are this lane's
   auto find = [&](int r0, int (&rows)[4]) {
@@ -677,22 +700,23 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     uint16_t* to = row_at(a.Y + n0 + 8 * q, row, a.pitch_y);
     const int c = n0 + 32 * h + 8 * q;
     if (row < 0) return;
-    if (full) *reinterpret_cast<uint4*>(to + 32 * h) = v;
+    if (n0 + kRegCols <= a.C) *reinterpret_cast<uint4*>(to + 32 * h) = v;
     else if (c < a.C) store_cols8(to - (n0 + 8 * q), c, a.C, v);
   };
   int rows[4];
   if (adapter < 0) {
     if (!busy) return;
-    for (int r0 = first, s = 0; r0 < count; r0 += 32 * RG, s = s + 1 == kStages ? 0 : s + 1) {
+    for (int r0 = first, s = 0; r0 < count && n0 < a.C; advance(n0, r0), s = s + 1 == kStages ? 0 : s + 1) {
       find(r0, rows);
       cp_async_wait<kStages - 1>();
       __syncwarp();
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) put(rows[k], h, piece(s, h, k));
+        for (int k = 0; k < 4; ++k)
+          if (!WALK || r0 + 8 * k < count) put(rows[k], h, piece(s, h, k));
       __syncwarp();
-      copy(r0 + 32 * RG * kStages, s);
+      copy(s);
     }
     return;
   }
@@ -743,19 +767,24 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
   find(first, rows);
   if constexpr (KS > 0) {
     if constexpr (GMN) {
-      load_b(0, 0, held[0]);
-      load_b(0, 1, held[1]);
+      load_b(n0, 0, 0, held[0]);
+      load_b(n0, 0, 1, held[1]);
     }
     load_a(rows, 0, 0, f[0]);
     load_a(rows, 0, 1, f[1]);
   }
-  for (int r0 = first, s = 0; r0 < count; r0 += 32 * RG, s = s + 1 == kStages ? 0 : s + 1) {
-    int next[4];
-    find(r0 + 32 * RG, next);
+  for (int r0 = first, s = 0; r0 < count && n0 < a.C; s = s + 1 == kStages ? 0 : s + 1) {
+    int next[4], nn = n0, nr = r0;
+    advance(nn, nr);
+    find(nr, next);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
+        if (WALK && m == 1 && r0 + 16 >= count) {  // no row in this half
+          if (nn != n0 && nn < a.C) load_b(nn, 0, h, held[h]);
+          break;
+        }
         float acc[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -769,11 +798,13 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
         };
         if constexpr (KS > 0) {
           product(f[m], held[h]);
-          if (h == 1) load_a(next, 0, m, f[m]);  // the next group's, as soon as the registers are free
+          // the next group's, as soon as the registers are free
+          if (h == 1 && !(WALK && count <= 32)) load_a(next, 0, m, f[m]);
+          if (WALK && m == 1 && nn != n0 && nn < a.C) load_b(nn, 0, h, held[h]);
         } else {
           for (int kb = 0; kb < (a.R + 31) / 32; ++kb) {
             load_a(rows, kb, m, f[0]);
-            load_b(kb, h, held[0]);
+            load_b(n0, kb, h, held[0]);
             product(f[0], held[0]);
           }
         }
@@ -783,6 +814,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          if (WALK && r0 + 16 * m + 8 * r >= count) break;
           uint4 x = piece(s, h, 2 * m + r);
           uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -795,7 +827,9 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
       }
     }
     __syncwarp();
-    copy(r0 + 32 * RG * kStages, s);
+    copy(s);
+    n0 = nn;
+    r0 = nr;
 #pragma unroll
     for (int k = 0; k < 4; ++k) rows[k] = next[k];
   }
@@ -1180,6 +1214,8 @@ int ring_stages(int budget, int stage) {
   return n > kMaxStages ? kMaxStages : n < 2 ? 2 : n;
 }
 
+constexpr int kShortRing = 50 * 1024;  // four blocks an SM
+
 // Maps, arguments and launch shape of a shrink; `budget` bytes of ring.
 template <bool GMN>
 struct ShrinkPlan {
@@ -1194,18 +1230,29 @@ struct ShrinkPlan {
     ok = rows_maps(&tmT, &tmT1, T, D, M, ldt, 128) &&
          (GMN ? make_tmap_3d(&tmG, G, R, D, L, 64, rowb) : make_tmap_3d(&tmG, G, D, R, L, Rn, 128));
     const int gbytes = GMN ? 64 * rowb * (R > 64 ? 2 : 1) : Rn * 128;
-    const int stage = kTile * 128 + gbytes;
-    const int stages = ring_stages(budget, stage);
-    // blocks of a cluster: as many as let every tile of full groups be resident
-    // at once with two blocks an SM, each with at least two steps of its own
-    // (shrink of [8192, 4096], rank 16, alone: 17 us with 4, 20 us with 2 or 8)
-    const int64_t nkb = (D + 63) / 64, busy = (M + kTile - 1) / kTile;
+    const int trows = M < kTile ? (int(M) + 31) / 32 * 32 : kTile;
+    const int stage = trows * 128 + gbytes;
+    // blocks of a cluster: as many as let every tile that is expected to have rows
+    // be resident at once with two blocks an SM, each with at least two steps of
+    // its own (shrink of [8192, 4096], rank 16, alone: 17 us with 4, 20 us with 2 or 8)
+    const int64_t nkb = (D + 63) / 64;
+    const int64_t busy = M < 64 * L ? (M < L ? M : L) + M / kTile : (M + kTile - 1) / kTile;
     tiles = max_tiles(M, L);
     cs = 1;
     while (cs < 8 && busy * 2 * cs <= 2 * sm_count() && nkb >= 4 * cs) cs *= 2;
-    const int ring = stages * stage, part = kTile * (int(R) + 4) * 4;
+    // small stages: twice as many blocks an SM with shorter rings (a row each of 64
+    // adapters, K = 4096, rank 16: 19 us with the expand, 26 with long rings)
+    if (cs < 8 && budget > kShortRing && trows < kTile && nkb >= 4 * cs && busy * 2 * cs <= 4 * sm_count()) {
+      cs *= 2;
+      budget = kShortRing;
+    }
+    // the same where the adapters' last tiles may make them more than two blocks an
+    // SM ([8192, 4096], 32 adapters in no order: 31 us, with long rings 42)
+    if (budget > kShortRing && M >= 64 * L && (busy + L) * cs > 2 * sm_count()) budget = kShortRing;
+    const int stages = ring_stages(budget, stage);
+    const int ring = ring_of(stages, stage), part = kTile * (int(R) + 4) * 4;
     smem = (ring > part ? ring : part) + kBarBytes + 1024;
-    a = ShrinkArgs{plan, scale, P, ldp, int(M), int(D), int(R), stages, gbytes, rowb, err};
+    a = ShrinkArgs{plan, scale, P, ldp, int(M), int(D), int(R), stages, trows, gbytes, rowb, err};
   }
 };
 
@@ -1229,8 +1276,8 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
                   int64_t ldb, void* Y, int64_t ldy, int64_t M, int64_t C, int64_t R, int64_t L, uint32_t* err,
                   cudaStream_t st) {
   const ExpandRegArgs a{plan, scale, static_cast<const uint16_t*>(P), static_cast<const uint16_t*>(G),
-                        static_cast<const uint16_t*>(base), static_cast<uint16_t*>(Y), uint32_t(ldp * 2), uint32_t(ldb * 2),
-                        uint32_t(ldy * 2), int(C), int(R)};
+                        static_cast<const uint16_t*>(base), static_cast<uint16_t*>(Y), uint32_t(ldp * 2),
+                        uint32_t(ldb * 2), uint32_t(ldy * 2), int(C), int(R)};
   const unsigned tiles = unsigned(max_tiles(M, L));
   if (R > 32 && M >= 64 * L) {
     const int smem = (kTile + kTcCols) * 128 + kBarBytes + 1024;
@@ -1247,26 +1294,37 @@ spg_status expand(const void* P, int64_t ldp, const void* G, const float* scale,
     kern<<<dim3(unsigned((blocks + span - 1) / span), tiles), dim3(128), smem, st>>>(ta);
     return launch_status();
   }
-  // Few whole tiles: their groups of 32 rows go to warps side by side (M 1024,
-  // C 4096: 16.0 against 17.4 us with a group after the other); otherwise a warp
-  // takes them in turn and keeps G ([8192, 16384]: 103 against 112 us; 16 rows of
-  // 8 adapters: 10.5 against 14.8).
+  // Few whole tiles: their groups of 32 rows go to warps side by side ([2048, 2048],
+  // rank 16, behind a small shrink: 9.3 against 12.5 us); otherwise a warp takes them in turn and
+  // keeps G ([2048, 4096] 15.4 against 15.8 us, above that no difference).
   const int64_t busy = M / kTile * ((C + 255) / 256);
-  auto go = [&](auto shape) -> spg_status {
-    constexpr int RG = decltype(shape)::value;
-    using Sh = RegShape<RG>;
-    auto kern = R <= 16   ? expand_reg_kernel<BF16, GMN, 1, RG>
-                : R <= 32 ? expand_reg_kernel<BF16, GMN, 2, RG>
-                          : expand_reg_kernel<BF16, GMN, 0, RG>;
+  auto go = [&](auto kern, auto shape, int64_t span) -> spg_status {
+    using Sh = decltype(shape);
     const int smem = Sh::BASE + (GMN ? (R <= 16 ? 16 : (int(R) + 31) / 32 * 32) * Sh::PITCH : 0);
     if (prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
-    return launch_pdl(kern, dim3(unsigned((C + Sh::COLS - 1) / Sh::COLS), tiles), dim3(Sh::THREADS), smem, st, a) ==
+    const int64_t blocks = (C + Sh::COLS - 1) / Sh::COLS;
+    return launch_pdl(kern, dim3(unsigned((blocks + span - 1) / span), tiles), dim3(Sh::THREADS), smem, st, a) ==
                    cudaSuccess
                ? launch_status()
                : SPG_ERR_CUDA;
   };
-  return M >= 64 * L && busy > 0 && busy < 2 * sm_count() ? go(std::integral_constant<int, 4>())
-                                                          : go(std::integral_constant<int, 1>());
+  if (R > 32) return go(expand_reg_kernel<BF16, GMN, 0, 1, false>, RegShape<1>(), 1);
+  if (M >= 64 * L && busy > 0 && busy < 2 * sm_count())
+    return go(R <= 16 ? expand_reg_kernel<BF16, GMN, 1, 4, false> : expand_reg_kernel<BF16, GMN, 2, 4, false>,
+              RegShape<4>(), 1);
+  if constexpr (!GMN) {
+    if (M < 64 * L) {
+      // a row each of 64 adapters, C 16384, rank 16: 14.0 us with three blocks of columns a
+      // block, 14.2 with six, 16.0 with eight, 16.5 with one
+      const int64_t groups = M < L ? M : L;
+      int64_t span = groups * ((C + 255) / 256) / (8 * sm_count());
+      span = span < 1 ? 1 : span > 8 ? 8 : span;
+      return go(R <= 16 ? expand_reg_kernel<BF16, GMN, 1, 1, true> : expand_reg_kernel<BF16, GMN, 2, 1, true>,
+                RegShape<1>(), span);
+    }
+  }
+  return go(R <= 16 ? expand_reg_kernel<BF16, GMN, 1, 1, false> : expand_reg_kernel<BF16, GMN, 2, 1, false>,
+            RegShape<1>(), 1);
 }
 
 // Adapters that can have whole tiles of rows.
@@ -1316,7 +1374,7 @@ template <bool BF16>
 spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale, const Plan& plan, void* U,
                 const void* V, int64_t ldv, void* dB, int64_t M, int64_t N, int64_t R, int64_t L, uint32_t* err,
                 cudaStream_t st) {
-  const ShrinkPlan<true> s(dY, lddy, B, scale, plan, U, R, M, N, R, L, 50 * 1024, err);
+  const ShrinkPlan<true> s(dY, lddy, B, scale, plan, U, R, M, N, R, L, kShortRing, err);
   const WgradPlan w(dY, lddy, V, ldv, scale, plan, dB, M, N, R, L, 50 * 1024, err);
   auto kern = dual_kernel<BF16>;
   const int smem = s.smem > w.smem ? s.smem : w.smem;
@@ -1341,8 +1399,9 @@ spg_status validate(const void* X, int64_t ldx, const void* A, const void* B, co
   if (M < 0 || N <= 0 || K <= 0 || R <= 0 || L <= 0 || ldx < K || ldv < R) return SPG_ERR_INVALID_ARG;
   if (!A || !B || (M != 0 && (!X || !V || !plan))) return SPG_ERR_INVALID_ARG;
   if (K % 8 || R % 8 || R > kMaxR || L > kMaxL) return SPG_ERR_UNSUPPORTED_SHAPE;
-  const int64_t lim = int64_t(1) << 31;
-  if (M >= (int64_t(1) << 22) || N >= lim - 256 || K >= lim - 256) return SPG_ERR_UNSUPPORTED_SHAPE;
+  if (M >= (int64_t(1) << 22) || N >= kMaxPitch - 256 || K >= kMaxPitch - 256 || ldx >= kMaxPitch ||
+      ldv >= kMaxPitch)
+    return SPG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(scale, 4) || !aligned(plan, 16)) return SPG_ERR_MISALIGNED;
   if (M != 0 && (!mat_ok(X, ldx) || !mat_ok(V, ldv))) return SPG_ERR_MISALIGNED;
   return SPG_OK;
@@ -1417,6 +1476,7 @@ spg_status lora_f16(const void* X, int64_t ldx, const void* A, const void* B, co
   if (rc != SPG_OK) return rc;
   if (ldy < N || (base && ldbase < N) || (M != 0 && !Y) || (base == Y && base && ldbase != ldy))
     return SPG_ERR_INVALID_ARG;
+  if (ldy >= kMaxPitch || (base && ldbase >= kMaxPitch)) return SPG_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return SPG_OK;
   if (!mat_ok(Y, ldy) || (base && !mat_ok(base, ldbase))) return SPG_ERR_MISALIGNED;
   rc = check_device();
@@ -1448,6 +1508,8 @@ spg_status lora_f16_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx
   if (lddy < N || !dA || !dB || (dX && lddx < K) || (dX && dbase && lddbase < K) ||
       (dX && dX == dbase && lddx != lddbase))
     return SPG_ERR_INVALID_ARG;
+  if (lddy >= kMaxPitch || (dX && lddx >= kMaxPitch) || (dX && dbase && lddbase >= kMaxPitch))
+    return SPG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(dA, 16) || !aligned(dB, 16)) return SPG_ERR_MISALIGNED;
   auto st = reinterpret_cast<cudaStream_t>(stream);
   if (M == 0) {  // no rows: the sums over them are zero

@@ -155,6 +155,15 @@ def test_lora_argument_errors(f):
         assert f(lddx=68) == MISALIGNED and f(dbase=24, lddbase=64) == MISALIGNED and f(ws=24) == MISALIGNED
 
 
+def test_lora_pitch_limits():
+    big = 1 << 31
+    for k in (dict(ldx=big), dict(ldv=big), dict(ldy=big), dict(base=32, ldbase=big), dict(N=big - 256, ldy=big - 8)):
+        assert _lora(**k) == SHAPE, k
+    for k in (dict(ldx=big), dict(ldv=big), dict(lddy=big), dict(lddx=big), dict(dbase=32, lddbase=big)):
+        assert _lorab(**k) == SHAPE, k
+    assert _lorab(dX=None, lddx=big, dY=None) == INVALID  # a pitch that is not used; the call fails for its dY
+
+
 def test_lora_plan_errors_and_sizes():
     L = spg.lib()
     assert L.lora_plan_size(-1, 2) == 0 and L.lora_plan_size(4, 0) == 0 and L.lora_plan_size(4, 8193) == 0
