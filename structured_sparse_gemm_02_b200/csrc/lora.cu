@@ -777,12 +777,17 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     int next[4], nn = n0, nr = r0;
     advance(nn, nr);
     find(nr, next);
+    // the next group's operands, as soon as their registers are free
+    auto ahead = [&](int h, int m) {
+      if (h == 1 && !(WALK && count <= 32)) load_a(next, 0, m, f[m]);
+      if (WALK && m == 1 && nn != n0 && nn < a.C) load_b(nn, 0, h, held[h]);
+    };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (WALK && m == 1 && r0 + 16 >= count) {  // no row in this half
-          if (nn != n0 && nn < a.C) load_b(nn, 0, h, held[h]);
+        if (WALK && m == 1 && r0 + 16 >= count) {  // no row in this half: only the next group's reads
+          ahead(h, 1);
           break;
         }
         float acc[4][4];
@@ -798,9 +803,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
         };
         if constexpr (KS > 0) {
           product(f[m], held[h]);
-          // the next group's, as soon as the registers are free
-          if (h == 1 && !(WALK && count <= 32)) load_a(next, 0, m, f[m]);
-          if (WALK && m == 1 && nn != n0 && nn < a.C) load_b(nn, 0, h, held[h]);
+          ahead(h, m);
         } else {
           for (int kb = 0; kb < (a.R + 31) / 32; ++kb) {
             load_a(rows, kb, m, f[0]);

@@ -309,3 +309,30 @@ def test_gradients_against_differences():
             want[j] = loss(*hi) - loss(*lo)
         off = (g.double().flatten() - want).norm()
         assert off <= 3 * 2.0 ** -11 * want.norm()
+
+
+@pytest.mark.parametrize("M,N,K,R,L,dt", [(200, 5001, 264, 16, 64, "bf16"), (130, 9000, 72, 24, 40, "f16"),
+                                          (64, 16384, 128, 32, 64, "bf16"), (33, 20000, 520, 8, 300, "f16"),
+                                          (97, 2000, 1032, 128, 64, "bf16"), (127, 700, 2056, 56, 3, "f16"),
+                                          (500, 4099, 1024, 16, 33, "bf16"), (5, 30001, 8, 16, 500, "bf16")])
+def test_few_rows_in_skewed_groups(M, N, K, R, L, dt):
+    """Fewer than 64 rows an adapter, but most of them on one: groups of one row, of several tiles, and none."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    p = _problem(M, N, K, R, L, _dt(dt), none=0.1, seed=21)
+    p["index"][: 2 * M // 3] = L // 2
+    p["index"][M // 4: M // 3] = -1
+    plan = spg.lora_plan(p["index"], L)
+    Y, V = spg.lora_f16(p["X"], p["A"], p["B"], plan, scale=p["scale"], base=p["base"])
+    _check_forward(p, Y, V)
+    rows = torch.empty_strided(p["base"].shape, p["base"].stride(), dtype=_dt(dt), device="cuda")
+    rows.copy_(p["base"])
+    spg.lora_f16(p["X"], p["A"], p["B"], plan, scale=p["scale"], base=rows, Y=rows)
+    assert torch.equal(rows, Y)
+    Y0, V0 = spg.lora_f16(p["X"], p["A"], p["B"], plan, scale=p["scale"])
+    assert torch.equal(V0, V)
+    _check_forward(dict(p, base=None), Y0, V0)
+    dX, dA, dB = spg.lora_f16_bwd(p["dY"], p["X"], V, p["A"], p["B"], plan, scale=p["scale"], dbase=p["dbase"])
+    _check_backward(p, V, dX, dA, dB)
+    assert spg.check_device_error() == 0
