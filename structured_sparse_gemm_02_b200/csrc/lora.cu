@@ -1372,19 +1372,29 @@ spg_status wgrad(const void* T, int64_t ldt, const void* P, int64_t ldp, const f
              : SPG_ERR_CUDA;
 }
 
-// U = s dY B_l and dB = s dY^T V from one reading of dY.
+// U = s dY B_l and dB = s dY^T V, from one reading of dY unless it has few columns:
+// then the sums over rows need many more blocks a unit than those over columns,
+// and two launches do better (backward of [5692, 144], rank 128: 80 against 169 us;
+// with twice as many [1970, 1000], rank 8: 31 against 23 us).
 template <bool BF16>
 spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale, const Plan& plan, void* U,
                 const void* V, int64_t ldv, void* dB, int64_t M, int64_t N, int64_t R, int64_t L, uint32_t* err,
                 cudaStream_t st) {
   const ShrinkPlan<true> s(dY, lddy, B, scale, plan, U, R, M, N, R, L, kShortRing, err);
   const WgradPlan w(dY, lddy, V, ldv, scale, plan, dB, M, N, R, L, 50 * 1024, err);
+  if (w.cs >= 4 * s.cs) {
+    const spg_status rc = shrink<BF16, true>(dY, lddy, B, scale, plan, U, R, M, N, R, L, err, st);
+    return rc != SPG_OK ? rc : wgrad<BF16, false>(dY, lddy, V, ldv, scale, plan, dB, M, N, R, L, err, st);
+  }
   auto kern = dual_kernel<BF16>;
   const int smem = s.smem > w.smem ? s.smem : w.smem;
   if (!s.ok || !w.ok || prepare(kern, smem) != SPG_OK) return SPG_ERR_CUDA;
   const int64_t units = (w.blocks + s.cs - 1) / s.cs * s.cs * L;
-  // a unit's rows are split over the cluster only where the units do not fill the device
-  const int parts = w.blocks * row_groups(M, L) < sm_count() ? s.cs : 1;
+  // a unit's rows are split over the cluster only where the units do not fill the
+  // device and most blocks have rows (backward of 11 rows of 16 adapters, N 13920:
+  // 38 us, split 189; [1970, 1000], 5 adapters: split over 8 blocks 23 us, 31 in one)
+  const int64_t groups = row_groups(M, L);
+  const int parts = w.blocks * groups < sm_count() && M / groups >= 32 * s.cs ? s.cs : 1;
   const int64_t clusters = s.tiles + (parts > 1 ? units : (units + s.cs - 1) / s.cs);
   return launch_pdl_cluster(kern, dim3(unsigned(clusters * s.cs)), dim3(128), smem, s.cs, st, s.tmT, s.tmT1, s.tmG,
                             w.tmP, w.tmP1, s.a, w.a, int(s.tiles), int(w.blocks), int(L), parts) == cudaSuccess
