@@ -1176,9 +1176,9 @@ __global__ void __launch_bounds__(128) wgrad_kernel(const __grid_constant__ CUte
 // so that whichever reads a part of dY second finds it in L2.  Where there are
 // units enough (parts == 1) each block of a cluster has one of its own: split
 // over the cluster, [2048, 16384] with 4 adapters took 74 us of 4096 blocks with
-// one chunk of rows each.  Bound by what comes out of L2, where both readers and the
-// rows of B and V meet: [8192, 16384] 79 us at rank 16, 98 us at rank 64, 316 MB
-// of them from DRAM (the matrix has 268).
+// one chunk of rows each.  [8192, 16384]: 79 us at rank 16, 90 us at rank 64, where 390 MB
+// come from DRAM (the matrix has 268); DRAM is busy 55 % of that time, L2
+// 40 %, and the blocks wait for their loads.
 template <bool BF16>
 __global__ void __launch_bounds__(128) dual_kernel(const __grid_constant__ CUtensorMap tmT,
                                                    const __grid_constant__ CUtensorMap tmT1,
