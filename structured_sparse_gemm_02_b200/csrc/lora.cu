@@ -19,10 +19,10 @@
 // are operands of the tensor cores; every sum is fp32.
 //
 // A block of a cluster may wait for tensor memory while another block of it
-// holds some, so such blocks of several streams must never use up an SM's tensor
-// memory between them: those of shrink, wgrad and dual take more than 520 bytes
-// of shared memory for each column (an SM has 456), and beside a block of the
-// pruned layers' kernels, which take nearly all of it, none fits.  Blocks of
+// holds some, so such blocks, of several streams too, must never use up an SM's
+// tensor memory between them: those of shrink, wgrad and dual take at least
+// kSmemPerColumn bytes of shared memory for each column.  Beside a block of the
+// pruned layers' kernels, which take nearly all of an SM's, none fits.  Blocks of
 // the expand kernels wait for no other block.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -258,13 +258,19 @@ __device__ __forceinline__ void ring_init(const Ring& r, uint32_t tmem_cols, int
   griddep_launch_dependents();
 }
 
-__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
 __host__ __device__ inline int round16(int r) { return (r + 15) & ~15; }
 // Tensor-memory columns for n accumulator columns: a power of two, at least 32.
 __host__ __device__ inline uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : 128u; }
+constexpr int kSmemPerColumn = 228 * 1024 / 512;  // of an SM, for 512 columns
+// Shared memory of a block with `bytes` of ring or sums and n accumulator columns.
+__host__ inline int block_smem(int bytes, int n) {
+  const int all = bytes + kBarBytes + 1024, least = int(tmem_cols(n)) * kSmemPerColumn;
+  return all > least ? all : least;
+}
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
 
 // The 128-byte-swizzled tiles below are rows of 64 elements (128 bytes), eight
 // rows to a 1024-byte group.  Read with the row as the MMA's M or N index they
@@ -1259,7 +1265,7 @@ struct ShrinkPlan {
     if (budget > kShortRing && M >= 64 * L && (busy + L) * cs > 2 * sm_count()) budget = kShortRing;
     const int stages = ring_stages(budget, stage);
     const int ring = ring_of(stages, stage), part = kTile * (int(R) + 4) * 4;
-    smem = (ring > part ? ring : part) + kBarBytes + 1024;
+    smem = block_smem(ring > part ? ring : part, round16(int(R)));
     a = ShrinkArgs{plan, scale, P, ldp, int(M), int(D), int(R), stages, trows, gbytes, rowb, err};
   }
 };
@@ -1358,7 +1364,7 @@ struct WgradPlan {
     cs = 1;
     while (cs < 8 && blocks * groups * cs < 2 * sm_count() && M / groups >= 64 * cs) cs *= 2;
     const int ring = stages * stage, part = kWgCols * (int(R) + 4) * 4;
-    smem = (ring > part ? ring : part) + kBarBytes + 1024;
+    smem = block_smem(ring > part ? ring : part, round16(int(R)));
     a = WgradArgs{plan, scale, dG, int(M), int(C), int(R), stages, rowb, err};
   }
 };

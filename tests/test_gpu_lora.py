@@ -336,3 +336,32 @@ def test_few_rows_in_skewed_groups(M, N, K, R, L, dt):
     dX, dA, dB = spg.lora_f16_bwd(p["dY"], p["X"], V, p["A"], p["B"], plan, scale=p["scale"], dbase=p["dbase"])
     _check_backward(p, V, dX, dA, dB)
     assert spg.check_device_error() == 0
+
+
+@pytest.mark.parametrize("M,K,R,L,dt", [(64, 4096, 72, 64, "bf16"), (30, 8192, 80, 60, "f16"), (96, 4096, 104, 96, "bf16"),
+                                        (64, 4096, 40, 64, "f16")])
+def test_few_rows_wide_ranks(M, K, R, L, dt):
+    """A tile an adapter with blocks that take much of an SM's tensor memory, on two streams at once."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    p = _problem(M, 1000, K, R, L, _dt(dt), none=0.0, seed=31)
+    p["index"].copy_(torch.arange(M, dtype=torch.int32) % L)
+    plan = spg.lora_plan(p["index"], L)
+
+    def step():
+        Y, V = spg.lora_f16(p["X"], p["A"], p["B"], plan, scale=p["scale"], base=p["base"])
+        return Y, V, *spg.lora_f16_bwd(p["dY"], p["X"], V, p["A"], p["B"], plan, scale=p["scale"], dbase=p["dbase"])
+    want = step()
+    _check_forward(p, *want[:2])
+    _check_backward(p, *want[1:])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(6):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(step())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for got in outs for a, b in zip(got, want))
+    assert spg.check_device_error() == 0
