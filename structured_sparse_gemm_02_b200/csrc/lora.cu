@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     expand_reg_kernel(const ExpandRegArgs a) {
   using Sh = RegShape<RG>;
   constexpr int kStages = Sh::STAGES;
+  constexpr bool kFew = WALK || KS == 0;  // most groups are short: what has no row is left out
   extern __shared__ __align__(128) uint8_t gsm[];
   const int warp = (threadIdx.x >> 5) % Sh::CG, lane = threadIdx.x & 31;
   const int first = 32 * ((threadIdx.x >> 5) / Sh::CG);  // this warp's first rows of the tile
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
       uint8_t* to = mine + s * 4096 + r1 * 128 + ((v ^ ((r1 & 1) << 2)) << 4);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (WALK && r0 + 4 * i >= count) break;
+        if (kFew && r0 + 4 * i >= count) break;
         const bool ok = r0 + 4 * i + r1 < count;
         cp_async16(to + 512 * i, row_at(from, ok ? rowid[r0 + 4 * i + r1] : rowid[r0], a.pitch_b), ok ? in : 0);
       }
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (!WALK || r0 + 8 * k < count) put(rows[k], h, piece(s, h, k));
+          if (!kFew || r0 + 8 * k < count) put(rows[k], h, piece(s, h, k));
       __syncwarp();
       copy(s);
     }
@@ -793,8 +794,8 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (WALK && m == 1 && r0 + 16 >= count) {  // no row in this half: only the next group's reads
-          ahead(h, 1);
+        if (kFew && m == 1 && r0 + 16 >= count) {  // no row in this half: only the next group's reads
+          if constexpr (KS > 0) ahead(h, 1);
           break;
         }
         float acc[4][4];
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(RegShape<RG>::THREADS, RG == 4 ? 2 : KS == 1 ?
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          if (WALK && r0 + 16 * m + 8 * r >= count) break;
+          if (kFew && r0 + 16 * m + 8 * r >= count) break;
           uint4 x = piece(s, h, 2 * m + r);
           uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
