@@ -112,13 +112,17 @@ def lib() -> ctypes.CDLL:
 
 _torch = None
 _FLOAT_CODES: dict = {}
+_device = None  # the current device's index
+_raw = None     # a device's current stream without a Stream object (3 us), where torch offers that
 
 
 def _tm():
     """torch, imported with the first call that needs it (the package itself also builds without it)."""
-    global _torch
+    global _torch, _device, _raw
     if _torch is None:
         import torch
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _FLOAT_CODES.update({torch.float16: SPG_F16, torch.bfloat16: SPG_BF16, torch.float32: SPG_F32})
         _torch = torch
     return _torch
@@ -131,11 +135,9 @@ def _check(fn: str, st: int) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        torch = _tm()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object (3 us) where torch offers that
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        stream = torch.cuda.current_stream()
+        if _raw is not None:
+            return _raw(_device())
+        stream = _tm().cuda.current_stream()
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -151,7 +153,7 @@ def _ptr(t) -> Optional[int]:
 def _on_device(t, name: str) -> None:
     """A tensor whose pointer goes to a kernel lives on the current CUDA device."""
     torch = _tm()
-    if t.is_cuda and t.get_device() == torch.cuda.current_device():
+    if t.is_cuda and t.get_device() == _device():
         return
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (it is on {t.device})")
