@@ -185,15 +185,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   else
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-template <bool BF16>
-__device__ __forceinline__ uint16_t pack1(float v) {
-  return static_cast<uint16_t>(pack2<BF16>(v, 0.f) & 0xFFFFu);
-}
-template <bool BF16>
-__device__ __forceinline__ float unpack1(uint16_t v) {
-  return unpack2<BF16>(v).x;
-}
-
 // Bounded wait that ignores the abort flag (teardown, and the one wait that everything else follows).
 __device__ __forceinline__ void tail_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
   int never = 0;
