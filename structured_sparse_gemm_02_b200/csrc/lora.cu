@@ -1473,7 +1473,8 @@ spg_status lora_plan(const int32_t* index, int64_t M, int64_t L, int32_t* plan, 
   warps = warps > 32 ? 32 : warps;
   warps = warps > need ? (need > 0 ? need : 1) : warps;
   const int smem = int(warps * G * 4);
-  if (smem > 48 * 1024 && prepare(plan_kernel, smem) != SPG_OK) return SPG_ERR_CUDA;
+  // the 48 KB that need no leave hold the kernel's static arrays too
+  if (smem > 40 * 1024 && prepare(plan_kernel, smem) != SPG_OK) return SPG_ERR_CUDA;
   // every group needs a thread of its own in the scan, every strip a warp
   const int64_t threads = ((G > warps * 32 ? G : warps * 32) + 31) / 32 * 32;
   if (launch_pdl(plan_kernel, dim3(1), dim3(unsigned(threads > 1024 ? 1024 : threads)), smem,
