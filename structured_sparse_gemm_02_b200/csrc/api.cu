@@ -110,14 +110,14 @@ cudaError_t allow_smem(const void* kern, int smem) {
   static Entry cache[256];
   static int used = 0;
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = taken(cudaGetDevice(&dev));
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   Entry* at = nullptr;
   for (int i = 0; i < used && !at; ++i)
     if (cache[i].k == kern && cache[i].dev == dev) at = &cache[i];
   if (at && at->smem >= smem) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = taken(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
   if (at) at->smem = smem;
   else if (used < 256) cache[used++] = Entry{kern, dev, smem};

@@ -1532,8 +1532,8 @@ spg_status lora_f16_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx
   if (M == 0) {  // no rows: the sums over them are zero
     rc = check_device();
     if (rc != SPG_OK) return rc;
-    if (cudaMemsetAsync(dA, 0, size_t(L) * R * K * 2, st) != cudaSuccess ||
-        cudaMemsetAsync(dB, 0, size_t(L) * N * R * 2, st) != cudaSuccess)
+    if (taken(cudaMemsetAsync(dA, 0, size_t(L) * R * K * 2, st)) != cudaSuccess ||
+        taken(cudaMemsetAsync(dB, 0, size_t(L) * N * R * 2, st)) != cudaSuccess)
       return SPG_ERR_CUDA;
     return SPG_OK;
   }
