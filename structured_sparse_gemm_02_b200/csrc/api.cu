@@ -3,7 +3,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <map>
 #include <mutex>
+#include <new>
+#include <utility>
 
 #include "gather.cuh"
 #include "host.cuh"
@@ -104,24 +107,25 @@ bool make_tmap_2d_swz(CUtensorMap* map, const void* base, int esize, uint64_t co
   return r == CUDA_SUCCESS;
 }
 
+// The limits live as long as the process, one for each kernel and device, and
+// only ever rise: between a call's limit and its launch another thread may set
+// one for a smaller launch of the same kernel.
 cudaError_t allow_smem(const void* kern, int smem) {
-  struct Entry { const void* k; int dev; int smem; };
   static std::mutex mu;
-  static Entry cache[256];
-  static int used = 0;
+  static std::map<std::pair<const void*, int>, int> limits;
   int dev = 0;
   cudaError_t e = taken(cudaGetDevice(&dev));
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
-  Entry* at = nullptr;
-  for (int i = 0; i < used && !at; ++i)
-    if (cache[i].k == kern && cache[i].dev == dev) at = &cache[i];
-  if (at && at->smem >= smem) return cudaSuccess;
-  e = taken(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  if (e != cudaSuccess) return e;
-  if (at) at->smem = smem;
-  else if (used < 256) cache[used++] = Entry{kern, dev, smem};
-  return cudaSuccess;
+  try {
+    int& limit = limits[{kern, dev}];
+    if (limit >= smem) return cudaSuccess;
+    e = taken(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (e == cudaSuccess) limit = smem;
+    return e;
+  } catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1,

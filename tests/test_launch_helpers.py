@@ -72,3 +72,21 @@ def test_a_failed_call_leaves_no_status_for_the_next_one(run):
   CHECK(spg::launch_pdl(kernel, dim3(1), dim3(32), 0, nullptr, 1) == cudaSuccess);
   CHECK(spg::allow_smem(reinterpret_cast<const void*>(kernel), 65536) == cudaSuccess);
 """)
+
+
+def test_shared_memory_limits_of_many_kernels_and_devices_never_fall(run):
+    """A limit is set once for each kernel and device, raised for a larger launch and never lowered."""
+    run(r"""
+  static char kernels[200];
+  for (device = 0; device < 8; ++device)
+    for (char& k : kernels) CHECK(spg::allow_smem(&k, 100000) == cudaSuccess);
+  CHECK(sets == 8 * 200);
+  for (device = 0; device < 8; ++device)
+    for (char& k : kernels) {
+      CHECK(spg::allow_smem(&k, 60000) == cudaSuccess);
+      CHECK(spg::allow_smem(&k, 100000) == cudaSuccess);
+    }
+  CHECK(lowered == 0 && sets == 8 * 200);
+  device = 3;
+  CHECK(spg::allow_smem(kernels + 150, 120000) == cudaSuccess && sets == 8 * 200 + 1);
+""")
