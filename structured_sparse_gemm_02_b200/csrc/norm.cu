@@ -826,9 +826,9 @@ __global__ void __launch_bounds__(32 * bwd_warps(sizeof(T), NV)) ln_bwd_warp_ker
       mu = a.mean[row + step];
       rstd = a.rstd[row + step];
     }
-    // every lane takes part in the sums, so after them the stage has been read
     const float m1 = warp_sum(f2_get(r.s1).x + f2_get(r.s1).y) * inv;
     const float m2 = warp_sum(f2_get(r.s2).x + f2_get(r.s2).y) * inv;
+    __syncwarp();  // every lane has read its part of the stage, dh too, before it is filled again
     if (lane == 0 && row + a.stages * step < a.M) fetch(row + a.stages * step, s);
     T* dx = static_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll

@@ -21,3 +21,28 @@ def test_first_plan_of_a_process(M, L):
     p = subprocess.run([sys.executable, "-c", f"from tests.test_gpu_lora import test_plan; test_plan({M}, {L})"],
                        cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("C,dt", [(512, "f16"), (768, "f16"), (1024, "bf16"), (1001, "f16"), (260, "f32"), (512, "f32")])
+def test_backward_through_many_turns_of_the_ring(C, dt):
+    """Rows of 33 to 128 vectors, tens of turns of every warp's ring with the residual path's gradient in it: a
+    stage that is filled before all of it has been read would change dX.  The same bits from run to run, in place too."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_norm import _dt, _gen, _half, _mat, _ref_bwd
+    dt, g, M = _dt(dt), _gen(C), 60000
+    ld = (C + 7) // 8 * 8
+    X, dY, dH = _mat(g, M, C, dt, 1.5, 0.25, ld), _mat(g, M, C, dt, 0.3, ld=ld), _mat(g, M, C, dt, 0.3, ld=ld)
+    gamma = 1 + 0.2 * torch.randn(C, generator=g, device="cuda")
+    _, _, mean, rstd = spg.layernorm(X, gamma, None, 1e-5, stats=True)
+    dX, dga, dbe = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH)
+    for i in range(0, M, 20000):  # in parts: the reference holds 64 bits
+        r = slice(i, i + 20000)
+        want, tol, *_ = _ref_bwd(dY[r], X[r], mean[r], rstd[r], gamma, dH[r])
+        assert torch.all((dX[r].double() - want).abs() <= tol + _half(want, dt))
+    for turn in range(8):
+        out = torch.empty_strided(dH.shape, dH.stride(), dtype=dt, device="cuda").copy_(dH) if turn % 2 else None
+        got = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH if out is None else out, dX=out)
+        assert all(torch.equal(a, b) for a, b in zip(got, (dX, dga, dbe)))
+    assert spg.check_device_error() == 0
