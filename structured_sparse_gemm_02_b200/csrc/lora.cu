@@ -71,9 +71,10 @@ inline Plan plan_view(const int32_t* p, int64_t M, int64_t L) {
 // Groups the rows by adapter, in one block.  Each warp takes a strip of
 // consecutive rows and counts its own occurrences of every adapter (lanes that
 // share one vote, the lowest adds), so the order of a group's rows does not
-// depend on timing.  Bound by latency: 8192 rows 5.4 us, 64 rows 2.4 us.
-__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* __restrict__ index, int M, int L, int warps,
-                                                    Plan p) {
+// depend on timing.  The kernel may start before the one that writes `index`
+// has ended, so index is not read as data that never changes (no __restrict__).
+// Bound by latency: 8192 rows 5.4 us, 64 rows 2.4 us.
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* index, int M, int L, int warps, Plan p) {
   extern __shared__ int cnt[];  // [warps][L + 1]
   __shared__ int2 wsum[32];
   __shared__ int2 carry;

@@ -46,3 +46,38 @@ def test_backward_through_many_turns_of_the_ring(C, dt):
         got = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH if out is None else out, dX=out)
         assert all(torch.equal(a, b) for a, b in zip(got, (dX, dga, dbe)))
     assert spg.check_device_error() == 0
+
+
+def test_plan_follows_the_kernel_that_writes_its_index():
+    """The index comes from a kernel of this library, which lets the plan's start before its own end: each plan
+    groups the values of its turn."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    M, N, K, L = 64, 256, 128, 40
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    W = torch.zeros(N, K, dtype=torch.int8, device="cuda")
+    W[:, 0] = torch.randint(0, L, (N,), generator=g, device="cuda")
+    W[:, 4] = torch.randint(0, L, (N,), generator=g, device="cuda")
+    Wv, meta = spg.sparse_compress_24(W)
+    picks = []  # the product of such rows is column 0 or column 4 of W
+    for c in (0, 4):
+        X = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+        X[:, c] = 1
+        X[1::3] = 0
+        picks.append(X)
+    rows = torch.empty(M, N, dtype=torch.int32, device="cuda")
+    want = []
+    for X in picks:
+        spg.spgemm_24_s8(X, Wv, meta, Y=rows, out_mode=spg.SPG_OUT_S32)
+        assert torch.equal(rows, X.int().sum(1)[:, None] * W[:, 0 if X is picks[0] else 4].int()[None])
+        want.append(torch.sort(rows.flatten(), stable=True)[1].int())
+    plans = [spg.lora_plan(rows.flatten(), L) for _ in range(50)]
+    torch.cuda.synchronize()
+    for i, plan in enumerate(plans):  # nothing else between the two calls
+        spg.spgemm_24_s8(picks[i % 2], Wv, meta, Y=rows, out_mode=spg.SPG_OUT_S32)
+        spg.lora_plan(rows.view(-1), L, plan=plan)
+    at = 4 + (L + 2 + 3) // 4 * 4
+    for i, plan in enumerate(plans):
+        assert torch.equal(plan.buf[at:at + M * N], want[i % 2]), i
