@@ -408,13 +408,14 @@ spg_status spgemm_tw_f16_noalloc(const void* X, int64_t ldx, const spg_tw_desc* 
  *   Y    [M, C] of `dtype`, pitch ldy; Yq int8 [M, C], pitch ldy
  *   mean, rstd fp32 [M]: mu and r of each row for layernorm_bwd, or NULL
  * H and Y may be the same memory as X or res (same pointer and pitch), but not
- * as each other; Yq is memory of its own.  layernorm_bwd, with z = (h - mu) r and g = dY gamma:
+ * as each other; Yq, mean and rstd are memory of their own.  layernorm_bwd, with z = (h - mu) r and g = dY gamma:
  *   dX = r (g - mean_c g - z mean_c(g z)) (+ dH), one rounding to `dtype`
  *   dgamma[c] = sum_m dY z,  dbeta[c] = sum_m dY, summed in fp32 in a fixed
  *   order, one rounding to wdtype
  *   X    the h that the norm was taken of (H where there was a residual)
  *   dH   [M, C] or NULL: the gradient that reaches h by the residual path
- *   dX   [M, C]; may be the same memory as dY or dH (same pointer and pitch)
+ *   dX   [M, C]; may be the same memory as dY, X or dH (same pointer and pitch);
+ *        no other output shares memory with an input or another output
  *   dgamma, dbeta [C] of wdtype; dbeta may be NULL.  M == 0 writes zeros.
  *   workspace 16-byte aligned, ws_bytes >= layernorm_bwd_workspace_size; its
  *   contents are scratch, and calls that may overlap need one each.

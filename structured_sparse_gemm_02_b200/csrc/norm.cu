@@ -1128,7 +1128,8 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
       !aligned(workspace, 16))
     return SPG_ERR_MISALIGNED;
   if (ws_bytes < layernorm_bwd_workspace_size(M, C, dtype)) return SPG_ERR_INVALID_ARG;
-  if (M != 0 && (other_pitch(dY, lddy, dX, lddx) || other_pitch(dH, lddh, dX, lddx))) return SPG_ERR_INVALID_ARG;
+  if (M != 0 && (other_pitch(dY, lddy, dX, lddx) || other_pitch(X, ldx, dX, lddx) || other_pitch(dH, lddh, dX, lddx)))
+    return SPG_ERR_INVALID_ARG;
   spg_status rc = check_device();
   if (rc != SPG_OK) return rc;
   auto st = reinterpret_cast<cudaStream_t>(stream);

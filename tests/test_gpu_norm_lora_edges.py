@@ -81,3 +81,24 @@ def test_plan_follows_the_kernel_that_writes_its_index():
     at = 4 + (L + 2 + 3) // 4 * 4
     for i, plan in enumerate(plans):
         assert torch.equal(plan.buf[at:at + M * N], want[i % 2]), i
+
+
+@pytest.mark.parametrize("M,C,dt", [(300, 64, "bf16"), (500, 768, "f16"), (500, 769, "f16"), (120, 4104, "bf16"), (40, 16384, "bf16"),
+                                    (30, 12345, "f32"), (77, 1001, "f32")])
+def test_norm_backward_in_place_of_its_input(M, C, dt):
+    """dX over X, as over dY and dH: the bits of a call with memory of its own, with rows of every kind of kernel."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_norm import _dt, _gen, _mat
+    dt, g = _dt(dt), _gen(M + C)
+    for ld in (C, (C + 7) // 8 * 8):
+        X, dY, dH = (_mat(g, M, C, dt, 0.5, ld=ld) for _ in range(3))
+        gamma = 1 + 0.2 * torch.randn(C, generator=g, device="cuda")
+        _, _, mean, rstd = spg.layernorm(X, gamma, None, 1e-5, stats=True)
+        want = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH)
+        for place in (X, dY, dH):
+            kept = place.clone()
+            got = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH, dX=place)
+            assert got[0] is place and all(torch.equal(a, b) for a, b in zip(got, want))
+            place.copy_(kept)
