@@ -477,6 +477,9 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
  *   dA    [L, R, K], dB [L, N, R], contiguous, written whole
  *   workspace 16-byte aligned, ws_bytes >= lora_bwd_workspace_size; scratch,
  *         calls that may overlap need one each
+ * Y may share memory with X, and dX with dY, X or V (they are written when those
+ * have been read); no other output than those named above and the ones in place
+ * shares memory with an input or another output.
  * Limits: K % 8 == 0, R % 8 == 0, R <= 128, 1 <= L <= 8192, M < 2^22; N >= 1
  * (any); N and K below 2^31 - 256, pitches below 2^31.  X, V, base, Y, dY, dbase, dX 16-byte aligned with pitches that are
  * multiples of 8; A, B, dA, dB, plan 16-byte aligned.  M == 0 is valid:

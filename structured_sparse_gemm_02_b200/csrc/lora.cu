@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include "gather.cuh"
@@ -1406,6 +1407,14 @@ spg_status dual(const void* dY, int64_t lddy, const void* B, const float* scale,
              : SPG_ERR_CUDA;
 }
 
+// One of `outs` is the memory of one of `ins`.
+bool any_same(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o && o == i) return true;
+  return false;
+}
+
 bool mat_ok(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 // Sizes, pointers and alignment that the forward and backward calls share.
@@ -1497,6 +1506,8 @@ spg_status lora_f16(const void* X, int64_t ldx, const void* A, const void* B, co
   if (ldy >= kMaxPitch || (base && ldbase >= kMaxPitch)) return SPG_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return SPG_OK;
   if (!mat_ok(Y, ldy) || (base && !mat_ok(base, ldbase))) return SPG_ERR_MISALIGNED;
+  // V is written while X and A are read, and read while base is replaced by Y
+  if (any_same({V}, {X, A, B, base, Y}) || any_same({Y}, {A, B})) return SPG_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != SPG_OK) return rc;
   uint32_t* err = device_error_word();
@@ -1542,6 +1553,10 @@ spg_status lora_f16_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx
   if (!mat_ok(dY, lddy) || (dX && !mat_ok(dX, lddx)) || (dX && dbase && !mat_ok(dbase, lddbase)) ||
       !aligned(workspace, 16))
     return SPG_ERR_MISALIGNED;
+  // dB is written while dY, B and V are read, then dA while X is, and then dX while A is
+  if (any_same({dA, dB, workspace}, {dY, X, V, A, B, dbase, dX}) || any_same({dX}, {A, B}) ||
+      any_same({dB, workspace}, {dA}) || dB == workspace)
+    return SPG_ERR_INVALID_ARG;
   rc = check_device();
   if (rc != SPG_OK) return rc;
   uint32_t* err = device_error_word();

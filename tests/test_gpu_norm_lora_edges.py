@@ -102,3 +102,26 @@ def test_norm_backward_in_place_of_its_input(M, C, dt):
             got = spg.layernorm_bwd(dY, X, mean, rstd, gamma, dH=dH, dX=place)
             assert got[0] is place and all(torch.equal(a, b) for a, b in zip(got, want))
             place.copy_(kept)
+
+
+@pytest.mark.parametrize("M,K,R,L,dt", [(300, 264, 16, 3, "bf16"), (700, 512, 72, 4, "f16"), (40, 4096, 16, 40, "bf16")])
+def test_adapters_outputs_over_what_has_been_read(M, K, R, L, dt):
+    """Y over X, and dX over X or dY: square layers whose input is not needed any more."""
+    need_gpu()
+    import torch
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_lora import _dt, _problem
+    p = _problem(M, K, K, R, L, _dt(dt))
+    plan = spg.lora_plan(p["index"], L)
+    A, B, scale = p["A"], p["B"], p["scale"]
+    Y, V = spg.lora_f16(p["X"], A, B, plan, scale=scale, base=p["base"])
+    want = spg.lora_f16_bwd(p["dY"], p["X"], V, A, B, plan, scale=scale, dbase=p["dbase"])
+    for name in ("X", "dY"):
+        q = dict(p)
+        q[name] = torch.empty_strided(p[name].shape, p[name].stride(), dtype=_dt(dt), device="cuda").copy_(p[name])
+        if name == "X":
+            got, _ = spg.lora_f16(q["X"], A, B, plan, scale=scale, base=p["base"], Y=q["X"])
+            assert torch.equal(got, Y)
+            q["X"].copy_(p["X"])
+        got = spg.lora_f16_bwd(q["dY"], q["X"], V, A, B, plan, scale=scale, dbase=p["dbase"], dX=q[name])
+        assert got[0] is q[name] and all(torch.equal(a, b) for a, b in zip(got, want))
