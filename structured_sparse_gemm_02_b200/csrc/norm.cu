@@ -510,8 +510,9 @@ __device__ __forceinline__ void store_part(float* p, int C, int t, int threads, 
 // 2^lg lanes); the columns' sums stay in registers over all of them and go to
 // the block's own rows of `part` at the end, so the order of every sum is
 // fixed.  The next row's loads are issued before this row's sums.  Serves rows
-// of up to 32 vectors (bf16 [60000, 64] 11 us) and rows that are not 16-byte
-// aligned; those cost a load an element (bf16 [8192, 4097] 260 us).
+// of up to 32 vectors (bf16 [60000, 64] 11 us), fp32 rows of more than 8192
+// columns, and rows that are not 16-byte aligned; those cost a load an element
+// (bf16 [8192, 4097] 260 us).
 template <class T, int NV, bool VECTORS, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>()) ln_bwd_kernel(const BwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;
@@ -904,9 +905,9 @@ struct Shape {
   int threads;  // of the block
 };
 
-int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
+constexpr int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
 
-int lg_of(int nvec) {
+constexpr int lg_of(int nvec) {
   int lg = 0;
   while ((1 << lg) < nvec && lg < 5) ++lg;
   return lg;
@@ -914,7 +915,7 @@ int lg_of(int nvec) {
 
 // Up to four vectors a lane a row stays in one warp (no barrier); beyond that
 // a block with four vectors a thread, so that a row's two block sums weigh little.
-Shape fwd_shape(int C, int es) {
+constexpr Shape fwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
   if (nvec <= 128) return {true, lg_of(nvec), (nvec + 31) / 32, 128};
   return {false, 0, 4, round32((nvec + 3) / 4)};
@@ -922,7 +923,7 @@ Shape fwd_shape(int C, int es) {
 
 // One vector a lane where that holds the row (several rows a warp where it is
 // shorter); a warp with up to four a lane; otherwise two or four vectors a thread of a block.
-Shape bwd_shape(int C, int es) {
+constexpr Shape bwd_shape(int C, int es) {
   const int nvec = (C * es + 15) / 16;
   if (nvec <= 32) return {true, lg_of(nvec), 1, 256};
   if (nvec <= 128) {
@@ -935,7 +936,7 @@ Shape bwd_shape(int C, int es) {
 
 // Blocks of the backward kernel: as many as are resident, so that each leaves
 // one row of partial sums and no more, and a row group each at least.
-int bwd_per_sm(const Shape& s) {
+constexpr int bwd_per_sm(const Shape& s) {
   return s.lanes ? (s.nv == 1 ? 3 : 1) : s.threads > 256 ? 1 : s.threads > 128 ? 2 : 4;
 }
 int bwd_blocks(int64_t M, const Shape& s) {
@@ -947,18 +948,39 @@ int bwd_blocks(int64_t M, const Shape& s) {
 
 // The vectors of each thread that are whole and inside the row: all `nv`, all
 // but the last, or (0) none to be sure of.
-int sure_vectors(const Shape& s, int C, int es) {
+constexpr int sure_vectors(const Shape& s, int C, int es) {
   const int threads = s.lanes ? 1 << s.lg : s.threads, whole = C * es / 16;
   return whole >= threads * s.nv && C * es % 16 == 0 ? s.nv : whole >= threads * (s.nv - 1) ? s.nv - 1 : 0;
 }
 
+// Rows of `row_bytes` in a ring fit a block's share of shared memory at least twice.
+constexpr bool ring_fits(const Shape& s, int64_t row_bytes) {
+  return s.threads <= 512 && (224 * 1024 / bwd_per_sm(s) - 1024) / row_bytes >= 2;
+}
+
+// What the choices below rest on, for every row length: a row in a warp's lanes,
+// and a row of the backward pass, leaves no vector but the last of a thread in
+// question, and 16-bit rows always fit the ring (with dh, three matrices).
+constexpr bool dealt_as_chosen(int es, int first, int last) {
+  for (int C = first; C <= last; ++C) {
+    const Shape f = fwd_shape(C, es), b = bwd_shape(C, es);
+    if (f.lanes && sure_vectors(f, C, es) < f.nv - 1) return false;
+    if (sure_vectors(b, C, es) < b.nv - 1) return false;
+    if (es == 2 && !b.lanes && !ring_fits(b, int64_t(C) * es / 16 * 16 * 3)) return false;
+  }
+  return true;
+}
+static_assert(dealt_as_chosen(2, 1, 8192) && dealt_as_chosen(2, 8193, kMaxC), "16-bit rows");
+static_assert(dealt_as_chosen(4, 1, 8192) && dealt_as_chosen(4, 8193, kMaxC), "fp32 rows");
+
 using FwdKernel = void (*)(const FwdArgs);
 template <class T, int NV, bool LANES>
 FwdKernel fwd_kernel(int sure) {
-  return sure == NV       ? ln_fwd_kernel<T, NV, NV, LANES>
-         : sure < 0       ? ln_fwd_kernel<T, NV, ELEMENTS, LANES>
-         : sure == NV - 1 ? ln_fwd_kernel<T, NV, NV - 1, LANES>
-                          : ln_fwd_kernel<T, NV, 0, LANES>;
+  if (sure == NV) return ln_fwd_kernel<T, NV, NV, LANES>;
+  if (sure < 0) return ln_fwd_kernel<T, NV, ELEMENTS, LANES>;
+  if constexpr (!LANES)
+    if (sure < NV - 1) return ln_fwd_kernel<T, NV, 0, LANES>;
+  return ln_fwd_kernel<T, NV, NV - 1, LANES>;
 }
 
 template <class T>
@@ -985,12 +1007,11 @@ cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, bool vectors, int64_t b
 using BwdKernel = void (*)(const BwdArgs);
 template <class T, int NV>
 BwdKernel ring_kernel(int sure, bool dh) {
-  return sure == NV       ? (dh ? ln_bwd_ring_kernel<T, NV, NV, true> : ln_bwd_ring_kernel<T, NV, NV, false>)
-         : sure == NV - 1 ? (dh ? ln_bwd_ring_kernel<T, NV, NV - 1, true> : ln_bwd_ring_kernel<T, NV, NV - 1, false>)
-                          : (dh ? ln_bwd_ring_kernel<T, NV, 0, true> : ln_bwd_ring_kernel<T, NV, 0, false>);
+  return sure == NV ? (dh ? ln_bwd_ring_kernel<T, NV, NV, true> : ln_bwd_ring_kernel<T, NV, NV, false>)
+                    : (dh ? ln_bwd_ring_kernel<T, NV, NV - 1, true> : ln_bwd_ring_kernel<T, NV, NV - 1, false>);
 }
 template <class T, int NV>
-BwdKernel warp_kernel(int sure, bool dh) {  // a warp's rows fill all but the last vector of a lane
+BwdKernel warp_kernel(int sure, bool dh) {
   return sure == NV ? (dh ? ln_bwd_warp_kernel<T, NV, NV, true> : ln_bwd_warp_kernel<T, NV, NV, false>)
                     : (dh ? ln_bwd_warp_kernel<T, NV, NV - 1, true> : ln_bwd_warp_kernel<T, NV, NV - 1, false>);
 }
@@ -1022,13 +1043,13 @@ cudaError_t launch_bwd(const BwdArgs& a, const Shape& s, bool vectors, int block
     k = s.nv == 2 ? warp_kernel<T, 2>(sure, dh) : s.nv == 3 ? warp_kernel<T, 3>(sure, dh) : warp_kernel<T, 4>(sure, dh);
   } else {
     // the ring, where at least two rows of it fit the block's share of shared memory
-    const int64_t stages = (224 * 1024 / bwd_per_sm(s) - 1024) / row;
-    if (vectors && s.threads <= 512 && stages >= 2) {
+    if (vectors && ring_fits(s, row)) {
+      const int64_t stages = (224 * 1024 / bwd_per_sm(s) - 1024) / row;
       b.stages = stages > 16 ? 16 : static_cast<int>(stages);
       smem = size_t(b.stages * row);
       k = s.nv == 2 ? ring_kernel<T, 2>(sure, dh) : ring_kernel<T, 4>(sure, dh);
-    } else if (vectors) {  // 32-bit rows of more than 8192 columns
-      k = ln_bwd_kernel<T, 4, true, false>;
+    } else if (sizeof(T) == 4 && vectors) {  // rows of more than 8192 columns
+      k = ln_bwd_kernel<float, 4, true, false>;
     } else {
       k = s.nv == 1   ? ln_bwd_kernel<T, 1, false, false>
           : s.nv == 2 ? ln_bwd_kernel<T, 2, false, false>
