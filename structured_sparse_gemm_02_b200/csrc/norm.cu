@@ -994,8 +994,10 @@ cudaError_t launch_fwd(const FwdArgs& a, const Shape& s, bool vectors, int64_t b
   // Large batches are not launched ahead of the previous kernel's end: an SM that
   // never idles keeps that kernel's share of shared memory (the pruned layers'
   // is nearly all of it), and the loads under way are limited by what it leaves
-  // to L1.  Behind such a layer, 16-bit rows with a residual: [8192, 4096] 60 against 73 us,
-  // [6304, 1024] 10 against 11, without a residual 7.2 against 6.4.
+  // to L1.  A square fp16 layer and the norm behind it, in plain order against ahead:
+  // [8192, 4096] 151 / 154 us, [4096, 4096] with a residual 97 / 100; at the limit no
+  // difference ([9456, 1024] with a residual 33.0 / 32.9, [6304, 1024] 26.2 / 26.2); below it
+  // [6304, 1024] without a residual 20.8 / 20.6, [12608, 768] 24.2 / 23.9.
   const int64_t read = int64_t(a.M) * a.C * sizeof(T) * (a.res ? 2 : 1);
   if (read > (int64_t(32) << 20)) {
     k<<<static_cast<unsigned>(blocks), s.threads, 0, st>>>(a);
@@ -1067,12 +1069,12 @@ bool vec_ok(const void* p, int64_t ld, int es) { return p == nullptr || (aligned
 
 bool is_act(int d) { return d == SPG_F16 || d == SPG_BF16 || d == SPG_F32; }
 
-// What the two forward entry points share.
 // An output in place of an input keeps its rows where they are.
 bool other_pitch(const void* in, int64_t ldin, const void* out, int64_t ldout) {
   return in && in == out && ldin != ldout;
 }
 
+// What the two forward entry points share.
 spg_status fwd(const void* X, int64_t ldx, const void* res, int64_t ldres, void* H, int64_t ldh, const void* gamma,
                const void* beta, float eps, void* Y, int64_t ldy, float* mean, float* rstd, int64_t M, int64_t C,
                int dtype, int wdtype, int s8, float qscale, cudaStream_t st) {
