@@ -558,8 +558,8 @@ def _new(shape, dtype, like, stream, pad=False):
         with _torch.cuda.stream(_on_stream(stream, like.device)):
             return _new(shape, dtype, like, None, pad)
     if shape == like.shape and dtype is like.dtype and like.is_contiguous() and not (
-            pad and (shape[1] * dtype.itemsize) % 16):
-        return _torch.empty_like(like)  # the cheapest way to say the same
+            pad and (shape[1] * dtype.itemsize) % 16) and (len(shape) != 2 or like.stride(0) >= shape[1]):
+        return _torch.empty_like(like)  # the cheapest way to say the same (a single row may have any stride)
     if pad:
         M, C = shape
         step = 16 // dtype.itemsize

@@ -125,3 +125,32 @@ def test_adapters_outputs_over_what_has_been_read(M, K, R, L, dt):
             q["X"].copy_(p["X"])
         got = spg.lora_f16_bwd(q["dY"], q["X"], V, A, B, plan, scale=scale, dbase=p["dbase"], dX=q[name])
         assert got[0] is q[name] and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def test_single_rows_and_parameters():
+    """One row cut out of other memory (whatever its strides say), parameters, inference mode."""
+    need_gpu()
+    torch = _torch()
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_lora import _problem
+    p = _problem(40, 72, 64, 8, 3, torch.float16, none=0.0)
+    gamma = torch.nn.Parameter(torch.ones(64, device="cuda"))
+    Y = spg.layernorm(p["X"], gamma)[0]
+    plan = spg.lora_plan(p["index"], 3)
+    out, V = spg.lora_f16(Y, p["A"], p["B"], plan, base=p["base"])
+    with torch.inference_mode():
+        for r in (0, 7, 39):
+            for row in (p["X"][r:r + 1], p["X"][r].clone().view(64, 1).t(), p["X"][r::40][:1]):
+                y = spg.layernorm(row, gamma)[0]
+                assert torch.equal(y[0], Y[r])
+                one = spg.lora_plan(p["index"][r:r + 1], 3)
+                a, b = torch.nn.Parameter(p["A"]), torch.nn.Parameter(p["B"])
+                got, v = spg.lora_f16(y, a, b, one, base=p["base"][r:r + 1])
+                # the sums of few rows may be split in another way
+                assert (got[0].double() - out[r].double()).abs().max() <= 2.0 ** -9 * out[r].abs().max()
+                assert (v[0].double() - V[r].double()).abs().max() <= 2.0 ** -9 * V[r].abs().max()
