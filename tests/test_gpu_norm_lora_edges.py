@@ -132,6 +132,83 @@ def _torch():
     return torch
 
 
+@pytest.mark.parametrize("C", [64, 100, 768, 1001, 4096, 4099])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_norm_of_views(C, dt):
+    """Weights, statistics and outputs that start anywhere inside their buffers, columns of wider buffers, the
+    residual that is X itself: the bits of the same call on memory of its own, and nothing beside the views written."""
+    need_gpu()
+    torch = _torch()
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_norm import _dt, _gen, _mat
+    dt, g, M = _dt(dt), _gen(C), 37
+    X, R, dY = (_mat(g, M, C, dt, 1.0) for _ in range(3))
+    gamma, beta = (torch.randn(C, generator=g, device="cuda").to(dt) for _ in range(2))
+    want = spg.layernorm(X, gamma, beta, residual=R, stats=True)
+    grads = spg.layernorm_bwd(dY, want[1], want[2], want[3], gamma)
+    codes = spg.layernorm_s8(X, gamma, beta, 20.0, residual=R)[0]
+
+    def inside(t, at):  # a copy of t whose first element is `at` into its buffer; behind it stays 7
+        buf = torch.full((t.numel() + at + 3,), 7, dtype=t.dtype, device="cuda")
+        buf[at:at + t.numel()].copy_(t.flatten())
+        return buf, buf[at:at + t.numel()].view(t.shape)
+
+    def columns(t, at):  # columns `at` .. of a wider buffer
+        buf = torch.full((M, C + at + 5), 7, dtype=t.dtype, device="cuda")
+        buf[:, at:at + C].copy_(t)
+        return buf, buf[:, at:at + C]
+
+    for at in (1, 3):
+        ga, be = inside(gamma, at)[1], inside(beta, at + 1)[1]
+        bufs = [columns(X, at) for _ in range(2)]
+        got = spg.layernorm(columns(X, at)[1], ga, be, residual=columns(R, at)[1], H=bufs[0][1], Y=bufs[1][1], stats=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        q = columns(torch.zeros_like(codes), at)
+        assert torch.equal(spg.layernorm_s8(X, ga, be, 20.0, residual=R, Yq=q[1])[0], codes)
+        mean, rstd = inside(want[2], at)[1], inside(want[3], at)[1]
+        dx, outs = columns(X, at), [inside(gamma, at), inside(gamma, at + 2)]
+        got = spg.layernorm_bwd(columns(dY, at)[1], want[1], mean, rstd, ga, dX=dx[1], dgamma=outs[0][1], dbeta=outs[1][1])
+        # rows that are not aligned may be summed in another order
+        for a, b, c in zip(got, grads, (1, M, M)):
+            assert (a.double() - b.double()).abs().max() <= 2.0 ** -9 * b.double().abs().max(), c
+        for buf, view in bufs + [q, dx]:
+            assert bool((buf[:, :at] == 7).all()) and bool((buf[:, at + C:] == 7).all())
+        for buf, view in outs:
+            assert bool((buf[C + 8:] == 7).all()) and bool((buf[:at] == 7).all())
+    same = spg.layernorm(X, gamma, beta, residual=X)
+    place = X.clone()
+    got = spg.layernorm(place, gamma, beta, residual=place, H=place)
+    assert torch.equal(got[0], same[0]) and torch.equal(place, same[1])
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "current", "default handle"])
+def test_calls_on_streams_given_in_every_way(how):
+    """A stream object, its raw handle, the current stream and the default stream's handle: one result."""
+    need_gpu()
+    torch = _torch()
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_lora import _problem
+    p = _problem(200, 136, 264, 16, 3, torch.bfloat16)
+    gamma = torch.ones(264, device="cuda")
+
+    def step(stream):
+        plan = spg.lora_plan(p["index"], 3, stream=stream)
+        Y, _, mean, rstd = spg.layernorm(p["X"], gamma, None, stats=True, stream=stream)
+        out, V = spg.lora_f16(Y, p["A"], p["B"], plan, base=p["base"], stream=stream)
+        dY, dA, dB = spg.lora_f16_bwd(p["dY"], Y, V, p["A"], p["B"], plan, dbase=p["dbase"], stream=stream)
+        return (out, dA, dB) + spg.layernorm_bwd(dY, p["X"], mean, rstd, gamma, stream=stream)
+    want = step(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    if how == "current":
+        with torch.cuda.stream(s):
+            got = step(None)
+    else:
+        got = step({"stream": s, "handle": s.cuda_stream, "default handle": torch.cuda.default_stream().cuda_stream}[how])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_single_rows_and_parameters():
     """One row cut out of other memory (whatever its strides say), parameters, inference mode."""
     need_gpu()
