@@ -401,7 +401,8 @@ spg_status spgemm_tw_f16_noalloc(const void* X, int64_t ldx, const spg_tw_desc* 
  *                 of spgemm_24_s8 (whose scale[] carries 1 / qscale); a NaN
  *                 gives code 0
  * All sums and statistics are fp32, the variance from the differences to the
- * mean.  A NaN or infinity in a row stays in that row.
+ * mean.  A NaN or infinity in a row stays in that row, and a row's results are
+ * the same in a batch of any size.
  *   X    [M, C] of `dtype` (SPG_F16, SPG_BF16 or SPG_F32), pitch ldx >= C
  *   res  [M, C], pitch ldres, and H [M, C], pitch ldh: both or neither (NULL)
  *   gamma, beta [C] of wdtype, which is `dtype` or SPG_F32; beta may be NULL (0)
@@ -457,6 +458,10 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
  * get V = 0, Y = base and dX = dbase and take no part in the gradients; an
  * adapter without rows gets gradients of +0.  Results do not depend on timing,
  * nor does a row's or an adapter's result on what other rows or adapters hold.
+ * The sums over K and N are split into as many parts as M and L suggest, so the
+ * last bit of a row's V, U and what follows from them may differ between
+ * batches of other sizes.  U is internal; in fp16 its components lose bits
+ * below 2^-14 and vanish below 2^-25, as any fp16 gradient's do: scale the loss.
  *
  * lora_plan groups the rows by adapter on the device, for all calls on this
  * batch and these L adapters (every layer of the model, forward and backward):
@@ -481,8 +486,9 @@ spg_status layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ld
  * have been read); no other output than those named above and the ones in place
  * shares memory with an input or another output.
  * Limits: K % 8 == 0, R % 8 == 0, R <= 128, 1 <= L <= 8192, M < 2^22; N >= 1
- * (any); N and K below 2^31 - 256, pitches below 2^31.  X, V, base, Y, dY, dbase, dX 16-byte aligned with pitches that are
- * multiples of 8; A, B, dA, dB, plan 16-byte aligned.  M == 0 is valid:
+ * (any); N and K below 2^31 - 256, pitches below 2^31.  X, V, base, Y, dY,
+ * dbase, dX 16-byte aligned with pitches that are multiples of 8; A, B, dA, dB,
+ * plan 16-byte aligned.  M == 0 is valid:
  * lora_f16 does nothing, lora_f16_bwd writes zeros to dA and dB.
  * ------------------------------------------------------------------------- */
 size_t lora_plan_size(int64_t M, int64_t L); /* bytes; 0 for sizes outside the limits */

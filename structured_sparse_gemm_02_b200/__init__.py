@@ -569,7 +569,8 @@ def _new(shape, dtype, like, stream, pad=False):
 
 
 def _apart(**outs) -> None:
-    """The call's outputs do not share memory: each byte is written for one of them."""
+    """The call's outputs do not share memory: each byte is written for one of them.  Their
+    spans are compared, so columns of one buffer side by side are refused too."""
     spans = []
     for name, t in outs.items():
         if t is not None and t.numel():
@@ -578,7 +579,7 @@ def _apart(**outs) -> None:
     spans.sort()
     for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
         if start < end:
-            raise ValueError(f"{a} and {b} share memory")
+            raise ValueError(f"{a} and {b} share memory, or rows of one lie between rows of the other")
 
 
 def _ln_args(X, gamma):
@@ -634,7 +635,8 @@ def _ln_fwd(fn, X, gamma, beta, eps, qscale, residual, H, Y, ydt, stats, stream)
 def layernorm(X, gamma, beta=None, eps=1e-5, residual=None, H=None, Y=None, stats=False, stream=None):
     """Layer norm of X [M, C] (or of H = X + residual), fp16, bf16 or fp32; gamma and
     beta [C] in X's dtype or fp32.  Returns (Y, H, mean, rstd): H is None without a
-    residual, mean and rstd (fp32 [M], for layernorm_bwd) are None without ``stats``."""
+    residual, mean and rstd (fp32 [M], for layernorm_bwd) are None without ``stats``.
+    Outputs that the caller gives, here and in the calls below, take a stretch of memory each."""
     return _ln_fwd("layernorm", X, gamma, beta, eps, None, residual, H, Y, getattr(X, "dtype", None), stats, stream)
 
 

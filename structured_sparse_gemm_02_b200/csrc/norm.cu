@@ -326,9 +326,10 @@ __device__ __forceinline__ void ln_finish(const FwdArgs& a, f2 (&v)[NV][Vec<T>::
 
 // LANES: a row belongs to 2^lg lanes of a warp, otherwise to the block;
 // thread t of the row holds vectors t, t + threads, ... (NV of them).  Bound by
-// memory, and in short rows by the instructions of an element: bf16 [8192, 4096]
-// 26 us (5.2 TB/s), with a residual 52 us (5.2 TB/s), padded rows of 4097 40 us;
-// fp16 [12608, 768] 9.0 us, int8 codes of [6304, 1024] 6.4 us.
+// memory (bf16 [8192, 4096] 26 us, 5.2 TB/s; with a residual 52 us, 5.2 TB/s; fp32 47 us,
+// 5.8 TB/s; padded rows of 4097 40 us), and in short rows by the latency of a
+// block's own loads (fp16 [12608, 768] 9.0 us, 35 % of the issue slots; int8 codes
+// of [6304, 1024] 6.4 us).
 template <class T, int NV, int SURE, bool LANES>
 __global__ void __launch_bounds__(max_threads<T, NV>(), LANES || sizeof(T) == 4 ? 1 : 2) ln_fwd_kernel(const FwdArgs a) {
   constexpr int VE = Vec<T>::VE, VP = Vec<T>::VP;

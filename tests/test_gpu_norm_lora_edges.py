@@ -231,3 +231,23 @@ def test_single_rows_and_parameters():
                 # the sums of few rows may be split in another way
                 assert (got[0].double() - out[r].double()).abs().max() <= 2.0 ** -9 * out[r].abs().max()
                 assert (v[0].double() - V[r].double()).abs().max() <= 2.0 ** -9 * V[r].abs().max()
+
+
+@pytest.mark.parametrize("C,dt", [(64, "f16"), (768, "bf16"), (1001, "f16"), (4096, "bf16"), (4100, "f32"), (16384, "f16")])
+def test_a_row_of_the_norm_does_not_depend_on_its_batch(C, dt):
+    """Rows alone, in a small batch and in a large one: the same bits of Y, the statistics and dX."""
+    need_gpu()
+    torch = _torch()
+    import structured_sparse_gemm_02_b200 as spg
+    from tests.test_gpu_norm import _dt, _gen, _mat
+    dt, g, M = _dt(dt), _gen(C), 3000
+    ld = (C + 7) // 8 * 8
+    X, dY, dH = (_mat(g, M, C, dt, 1.0, ld=ld) for _ in range(3))
+    gamma = torch.randn(C, generator=g, device="cuda")
+
+    def both(rows):
+        Y, _, mean, rstd = spg.layernorm(X[rows], gamma, None, stats=True)
+        return Y, mean, rstd, spg.layernorm_bwd(dY[rows], X[rows], mean, rstd, gamma, dH=dH[rows])[0]
+    want = both(slice(0, M))
+    for rows in (slice(0, 1), slice(7, 8), slice(M - 1, M), slice(100, 117), slice(512, 1536)):
+        assert all(torch.equal(a, b[rows]) for a, b in zip(both(rows), want)), rows
